@@ -62,6 +62,31 @@ class _Mla(ctypes.Structure):
                 ("kv_row_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
+class _PagePlan(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_tok", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_free", ctypes.c_int32),
+                ("ctx_len", ctypes.c_void_p), ("new_len", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_begin", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("q_begin", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("q_seq", ctypes.c_void_p), ("q_pos", ctypes.c_void_p), ("slot_map", ctypes.c_void_p),
+                ("held_out", ctypes.c_void_p), ("free_used", ctypes.c_void_p)]
+
+
+class _PagedBatch(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_tok", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("q_begin", ctypes.c_void_p), ("seq_len", ctypes.c_void_p)]
+
+
+class _Verify(ctypes.Structure):
+    _fields_ = [("n_req", ctypes.c_int32), ("n_draft", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("target", ctypes.c_void_p), ("t_req_stride", ctypes.c_int64),
+                ("t_row_stride", ctypes.c_int64), ("draft", ctypes.c_void_p), ("d_req_stride", ctypes.c_int64),
+                ("d_row_stride", ctypes.c_int64), ("draft_tokens", ctypes.c_void_p), ("draft_len", ctypes.c_void_p),
+                ("accept_u", ctypes.c_void_p), ("sample_u", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("n_accept", ctypes.c_void_p)]
+
+
 _lib_handle = None
 
 
@@ -93,6 +118,12 @@ def lib():
         h.dsa_cache_writer_workspace_bytes.restype = SZ
         h.dsa_absorb_queries.argtypes = [I32, I32, P, P, P, P, ctypes.c_float, P, P, SZ, P]
         h.dsa_up_project.argtypes = [I32, I32, P, P, P, P, SZ, P]
+        h.dsa_page_tables.argtypes = [ctypes.POINTER(_PagePlan), P, SZ, P]
+        h.dsa_write_paged_rows.argtypes = [ctypes.POINTER(_CacheWriter), P, P, SZ, P]
+        h.dsa_paged_mla.argtypes = [ctypes.POINTER(_PagedBatch), ctypes.POINTER(_Mla), P, SZ, P]
+        h.dsa_paged_mla_workspace_bytes.argtypes = [ctypes.POINTER(_PagedBatch), ctypes.POINTER(_Mla)]
+        h.dsa_paged_mla_workspace_bytes.restype = SZ
+        h.dsa_verify_drafts.argtypes = [ctypes.POINTER(_Verify), P, SZ, P]
         h.dsa_workspace_bytes.argtypes = [I32, ctypes.POINTER(_Queries), I32, I32, I32, I32]
         h.dsa_workspace_bytes.restype = SZ
         h.dsa_workspace_init.argtypes = [P, SZ, P]
@@ -105,7 +136,8 @@ def lib():
                      "dsa_sparse_mla_mtp", "dsa_sparse_mla_decode_noalloc", "dsa_noalloc_check_status",
                      "dsa_indexshare_group", "dsa_indexshare_group_host", "dsa_workspace_init", "dsa_check_status",
                      "dsa_shard_candidates", "dsa_shard_merge", "dsa_shard_combine",
-                     "dsa_write_cache_rows", "dsa_absorb_queries", "dsa_up_project"):
+                     "dsa_write_cache_rows", "dsa_absorb_queries", "dsa_up_project",
+                     "dsa_page_tables", "dsa_write_paged_rows", "dsa_paged_mla", "dsa_verify_drafts"):
             getattr(h, name).restype = st
         _lib_handle = h
     return _lib_handle
@@ -225,7 +257,7 @@ class CacheWriter(_CStruct):
     rms_weight: torch.Tensor     # float32 [512]
     ln_weight: torch.Tensor      # float32 [128]
     ln_bias: torch.Tensor        # float32 [128]
-    tok_seq: torch.Tensor        # int32 [n_tok]
+    tok_seq: Optional[torch.Tensor]  # int32 [n_tok] (None for dsa_write_paged_rows)
     tok_pos: torch.Tensor        # int32 [n_tok]
     kv: Optional[torch.Tensor]   # bf16 [n_seq, L, 576] latent cache, or None
     k_idx: Optional[torch.Tensor]  # bf16 [n_seq, L, 128] indexer keys, or None
@@ -236,12 +268,85 @@ class CacheWriter(_CStruct):
         ref = self.kv if self.kv is not None else self.k_idx
         return _CacheWriter(self.h.shape[0], self.h.shape[1], self.h.data_ptr(), self.h.stride(0), self.w.data_ptr(),
                             self.rms_weight.data_ptr(), self.ln_weight.data_ptr(), self.ln_bias.data_ptr(),
-                            self.tok_seq.data_ptr(), self.tok_pos.data_ptr(), ref.shape[0], ref.shape[1],
+                            None if self.tok_seq is None else self.tok_seq.data_ptr(), self.tok_pos.data_ptr(),
+                            ref.shape[0], ref.shape[1],
                             None if self.kv is None else self.kv.data_ptr(),
                             0 if self.kv is None else self.kv.stride(0), 0 if self.kv is None else self.kv.stride(1),
                             None if self.k_idx is None else self.k_idx.data_ptr(),
                             0 if self.k_idx is None else self.k_idx.stride(0),
                             0 if self.k_idx is None else self.k_idx.stride(1), self.eps, self.rope_theta)
+
+
+def _int32(*tensors):
+    for t in tensors:
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+            raise TypeError(f"expected a contiguous int32 tensor, got {t.dtype} {tuple(t.shape)}")
+
+
+def _rows_int32(table: torch.Tensor):
+    if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise TypeError("the block table is int32 [n_seq, max_pages] with contiguous rows")
+
+
+def _dp(t: Optional[torch.Tensor]):
+    """Address of a tensor's first element, None for an empty tensor or none."""
+    return None if t is None or t.numel() == 0 else t.data_ptr()
+
+
+@dataclass
+class PagePlan(_CStruct):
+    """Arguments of dsa_page_tables; token count, table width and free list length
+    come from the tensors' shapes."""
+    ctx_len: torch.Tensor        # int32 [n_seq]
+    new_len: torch.Tensor        # int32 [n_seq]
+    held: torch.Tensor           # int32 [n_seq]
+    free_pages: torch.Tensor     # int32 [n_free]
+    free_begin: Optional[torch.Tensor]  # int32 [1], or None (0)
+    block_table: torch.Tensor    # int32 [n_seq, max_pages], written in place
+    q_begin: torch.Tensor        # int32 [n_seq + 1], output, like all below
+    seq_len: torch.Tensor        # int32 [n_seq]
+    q_seq: torch.Tensor          # int32 [n_tok]
+    q_pos: torch.Tensor          # int32 [n_tok]
+    slot_map: torch.Tensor       # int32 [n_tok]
+    held_out: torch.Tensor       # int32 [n_seq]
+    free_used: torch.Tensor      # int32 [1]
+    n_pages: int
+    page_rows: int
+
+    def _make(self) -> _PagePlan:
+        n, n_tok = self.ctx_len.numel(), self.q_seq.numel()
+        _int32(self.ctx_len, self.new_len, self.held, self.free_pages, self.free_begin, self.q_begin, self.seq_len,
+               self.q_seq, self.q_pos, self.slot_map, self.held_out, self.free_used)
+        _rows_int32(self.block_table)
+        if not (self.new_len.numel() == self.held.numel() == self.seq_len.numel() == self.held_out.numel() == n
+                and self.q_begin.numel() == n + 1 and self.block_table.shape[0] == n
+                and self.q_pos.numel() == self.slot_map.numel() == n_tok and self.free_used.numel() == 1):
+            raise ValueError("page plan: tensors of different lengths")
+        return _PagePlan(n, n_tok, self.n_pages, self.page_rows, self.block_table.shape[1], self.free_pages.numel(),
+                         _dp(self.ctx_len), _dp(self.new_len), _dp(self.held), _dp(self.free_pages),
+                         _dp(self.free_begin), _dp(self.block_table), self.block_table.stride(0), _dp(self.q_begin),
+                         _dp(self.seq_len), _dp(self.q_seq), _dp(self.q_pos), _dp(self.slot_map), _dp(self.held_out),
+                         _dp(self.free_used))
+
+
+@dataclass
+class PagedBatch(_CStruct):
+    """The tokens of a dsa_paged_mla call (Mla.kv is the pool [n_pages, page_rows, row])."""
+    block_table: torch.Tensor    # int32 [n_seq, max_pages]
+    q_begin: torch.Tensor        # int32 [n_seq + 1]
+    seq_len: torch.Tensor        # int32 [n_seq]
+    n_tok: int
+    n_pages: int
+    page_rows: int
+
+    def _make(self) -> _PagedBatch:
+        _int32(self.q_begin, self.seq_len)
+        _rows_int32(self.block_table)
+        n = self.seq_len.numel()
+        if self.q_begin.numel() != n + 1 or self.block_table.shape[0] != n:
+            raise ValueError("paged batch: tensors of different lengths")
+        return _PagedBatch(n, self.n_tok, self.n_pages, self.page_rows, self.block_table.shape[1],
+                           _dp(self.block_table), self.block_table.stride(0), _dp(self.q_begin), _dp(self.seq_len))
 
 
 # ------------------------------------------------------------------ entry points
@@ -409,10 +514,81 @@ def dsa_up_project(o_lat: torch.Tensor, w_uv: torch.Tensor, out: torch.Tensor, w
                                 ws.numel() * ws.element_size(), _stream(stream)), "dsa_up_project")
 
 
+def dsa_page_tables(plan: PagePlan, ws: torch.Tensor, stream=None):
+    pc = plan.c()
+    _check(lib().dsa_page_tables(ctypes.byref(pc), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "dsa_page_tables")
+
+
+def dsa_write_paged_rows(writer: CacheWriter, slot_map: torch.Tensor, ws: torch.Tensor, stream=None):
+    """writer.kv [n_pages, page_rows, 576] and writer.k_idx [n_pages, page_rows, 128]; slot_map int32 [n_tok]."""
+    _int32(slot_map)
+    wc = writer.c()
+    if slot_map.numel() != wc.n_tok:
+        raise ValueError("slot_map holds one slot per token")
+    if writer.kv is not None and writer.k_idx is not None and writer.kv.shape[:2] != writer.k_idx.shape[:2]:
+        raise ValueError("kv and k_idx hold the same pages and rows")
+    _check(lib().dsa_write_paged_rows(ctypes.byref(wc), _ptr(slot_map), _ptr(ws), ws.numel() * ws.element_size(),
+                                      _stream(stream)), "dsa_write_paged_rows")
+
+
+def _paged_shapes(batch: PagedBatch, mla: Mla):
+    kv = mla.kv
+    if kv.dim() != 3 or kv.shape[0] < batch.n_pages or kv.shape[1] < batch.page_rows:
+        raise ValueError("the pool is [n_pages, page_rows, row]")
+    if mla.q.shape[0] < batch.n_tok or mla.out.shape[0] < batch.n_tok or (mla.lse is not None and
+                                                                           mla.lse.shape[0] < batch.n_tok):
+        raise ValueError("queries and outputs hold n_tok rows")
+
+
+def dsa_paged_mla_workspace_bytes(batch: PagedBatch, mla: Mla) -> int:
+    return int(lib().dsa_paged_mla_workspace_bytes(ctypes.byref(batch.c()), ctypes.byref(mla.c())))
+
+
+def dsa_paged_mla(batch: PagedBatch, mla: Mla, ws: torch.Tensor, stream=None):
+    _paged_shapes(batch, mla)
+    bc, mc = batch.c(), mla.c()
+    _check(lib().dsa_paged_mla(ctypes.byref(bc), ctypes.byref(mc), _ptr(ws), ws.numel() * ws.element_size(),
+                               _stream(stream)), "dsa_paged_mla")
+
+
+def dsa_verify_drafts(target: torch.Tensor, draft_tokens: torch.Tensor, accept_u: torch.Tensor,
+                      sample_u: torch.Tensor, tokens: torch.Tensor, n_accept: torch.Tensor, ws: torch.Tensor,
+                      draft: Optional[torch.Tensor] = None, n_draft: Optional[torch.Tensor] = None, stream=None):
+    """target [n_req, D + 1, V], draft [n_req, D, V] or None (greedy drafts), draft_tokens int32 [n_req, D],
+    n_draft int32 [n_req] or None (D each), accept_u float32 [n_req, D], sample_u float32 [n_req] ->
+    tokens int32 [n_req, D + 1], n_accept int32 [n_req]."""
+    n, d1, v = target.shape
+    d = d1 - 1
+    _int32(draft_tokens, tokens, n_accept, n_draft)
+    if any(u.dtype != torch.float32 or not u.is_contiguous() for u in (accept_u, sample_u)):
+        raise TypeError("accept_u and sample_u are contiguous float32")
+    if (tuple(draft_tokens.shape) != (n, d) or tuple(accept_u.shape) != (n, d) or tuple(tokens.shape) != (n, d + 1)
+            or sample_u.numel() != n or n_accept.numel() != n or (n_draft is not None and n_draft.numel() != n)
+            or (draft is not None and tuple(draft.shape) != (n, d, v))):
+        raise ValueError("verify: tensors of different shapes")
+    if (v > 1 and target.stride(2) != 1) or (draft is not None and (draft.dtype != target.dtype or
+                                                                     (v > 1 and draft.numel() and draft.stride(2) != 1))):
+        raise TypeError("probability rows are contiguous and of one type")
+    vc = _Verify(n, d, v, _dtype_code(target), _dp(target), target.stride(0), target.stride(1), _dp(draft),
+                 0 if draft is None else draft.stride(0), 0 if draft is None else draft.stride(1), _dp(draft_tokens),
+                 _dp(n_draft), _dp(accept_u), _dp(sample_u), _dp(tokens), _dp(n_accept))
+    _check(lib().dsa_verify_drafts(ctypes.byref(vc), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "dsa_verify_drafts")
+
+
 # ------------------------------------------------------------------ conveniences
 def workspace(op: int, queries: Queries, topk: int = 1, n_layers: int = 1, device="cuda", stream=None):
     """Allocate (torch) and zero-initialise a workspace for `op`."""
     n = dsa_workspace_bytes(op, queries, topk, 64, 512, n_layers)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    dsa_workspace_init(ws, stream)
+    return ws
+
+
+def paged_workspace(batch: PagedBatch, mla: Mla, device="cuda", stream=None):
+    """Allocate (torch) and zero-initialise a workspace for dsa_paged_mla."""
+    n = dsa_paged_mla_workspace_bytes(batch, mla)
     ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
     dsa_workspace_init(ws, stream)
     return ws

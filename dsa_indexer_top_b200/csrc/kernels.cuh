@@ -50,6 +50,15 @@ cudaError_t set_max_dynamic_smem(void (*kernel)(KArgs...), int bytes) {
     return e;
 }
 
+// SMs of the current device.
+inline int sm_count_current() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+        return 148;
+    return n;
+}
+
 constexpr int kIdxHeads = 32;   // index_n_heads of GLM-5.2
 constexpr int kIdxDim = 128;    // index_head_dim of GLM-5.2
 constexpr int kMlaHeads = 64;   // num_attention_heads of GLM-5.2
@@ -237,6 +246,8 @@ struct CacheWriteArgs {
     int k_splits, n_tok;
     const float *rms_weight, *ln_weight, *ln_bias;
     const int32_t *tok_seq, *tok_pos;
+    const int32_t *slot_map;   // paged caches: row of token t (page * L + row of the page, n_seq
+                               // pages of L rows), -1 = none; null: row (tok_seq[t], tok_pos[t])
     void *kv;
     int64_t kv_seq_stride, kv_row_stride;
     void *k_idx;
@@ -258,6 +269,38 @@ struct QueryRopeArgs {
     double log2_theta;
 };
 cudaError_t launch_query_rope(const QueryRopeArgs &a, cudaStream_t st);
+
+// ------------------------------------------------------------------ paged caches
+struct PageTablesArgs {
+    dsa_page_plan p;
+    uint32_t *status;
+};
+cudaError_t launch_page_tables(const PageTablesArgs &a, int num_sms, cudaStream_t st);
+
+struct PagedMlaArgs {
+    const void *q;
+    const void *kv;
+    void *out;
+    float *lse;
+    int64_t kv_page_stride, kv_row_stride;  // elements; bytes for packed FP8 rows
+    const int32_t *block_table;
+    int64_t table_stride;
+    const int32_t *q_begin;
+    const int32_t *seq_len;
+    int n_seq, n_tok, n_pages, page_rows, max_pages;
+    int heads, d_lat, d_rope;
+    float scale;
+    int is_bf16, kv_fp8;
+    uint32_t *status;
+};
+cudaError_t launch_paged_mla_generic(const PagedMlaArgs &a, cudaStream_t st);
+
+// ------------------------------------------------------------------ draft verification
+struct VerifyArgs {
+    dsa_verify v;
+    uint32_t *status;
+};
+cudaError_t launch_verify(const VerifyArgs &a, int num_sms, cudaStream_t st);
 
 // ------------------------------------------------------------------ diagnostics
 // The limit of every device-side wait (the same value as kWaitLimitNs of the

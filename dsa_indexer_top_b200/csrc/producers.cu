@@ -58,8 +58,18 @@ __global__ void __launch_bounds__(kEpiThreads) cache_write_epilogue_kernel(const
     __shared__ float red[kEpiThreads / 32];
     const int t = blockIdx.x;
     griddep_wait();
-    const int seq = a.tok_seq[t], pos = a.tok_pos[t];
-    if (seq < 0 || seq >= a.n_seq || pos < 0 || pos >= a.L) {
+    const int pos = a.tok_pos[t];  // RoPE position
+    int seq, row_at;               // cache (or page) and row of it
+    if (a.slot_map) {
+        const int slot = a.slot_map[t];
+        if (slot == -1) return;  // padding: nothing to write
+        seq = slot >= 0 ? slot / a.L : -1;
+        row_at = pos < 0 ? -1 : slot - seq * a.L;
+    } else {
+        seq = a.tok_seq[t];
+        row_at = pos;
+    }
+    if (seq < 0 || seq >= a.n_seq || row_at < 0 || row_at >= a.L) {
         if (threadIdx.x == 0) report_status(a.status, DSA_ERR_INVALID);
         return;
     }
@@ -117,7 +127,7 @@ __global__ void __launch_bounds__(kEpiThreads) cache_write_epilogue_kernel(const
     const float rstd = 1.f / sqrtf(block_sum(sv, red) / kIdxDim + a.eps);
     if (a.kv) {
         __nv_bfloat16 *row = static_cast<__nv_bfloat16 *>(a.kv) + static_cast<int64_t>(seq) * a.kv_seq_stride +
-                             static_cast<int64_t>(pos) * a.kv_row_stride;
+                             static_cast<int64_t>(row_at) * a.kv_row_stride;
         for (int f = threadIdx.x; f < kLatent; f += kEpiThreads)
             row[f] = __float2bfloat16_rn(y[f] * rms * a.rms_weight[f]);
         if (threadIdx.x < kRope / 2) {
@@ -131,7 +141,7 @@ __global__ void __launch_bounds__(kEpiThreads) cache_write_epilogue_kernel(const
     }
     if (a.k_idx) {
         __nv_bfloat16 *key = static_cast<__nv_bfloat16 *>(a.k_idx) + static_cast<int64_t>(seq) * a.k_seq_stride +
-                             static_cast<int64_t>(pos) * a.k_row_stride;
+                             static_cast<int64_t>(row_at) * a.k_row_stride;
         const float *yk = y + kLatent + kRope;
         // dims 0..63 keep their normalised value; 64..127 (the RoPE part) are turned in pairs
         for (int f = threadIdx.x; f < kIdxDim - kRope; f += kEpiThreads)
@@ -193,7 +203,7 @@ size_t al256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // one CTA per SM on a 148-SM part, at least 4 blocks of 64 along K per split.
 void cache_plan(int n_tok, int hidden, int &m_tiles, int &k_splits, int &kb_per_split) {
     const int kb = (hidden + 63) / 64;
-    m_tiles = (n_tok + 127) / 128;
+    m_tiles = n_tok > 0 ? (n_tok + 127) / 128 : 1;
     const int tiles = m_tiles * ((kProjFeatures + 127) / 128);
     int s = 144 / tiles;
     s = s < 1 ? 1 : s;
@@ -232,10 +242,13 @@ size_t dsa_cache_writer_workspace_bytes(int32_t n_tok, int32_t hidden) {
     return cache_ws_bytes(n_tok, hidden);
 }
 
-dsa_status dsa_write_cache_rows(const dsa_cache_writer *cw, void *ws, size_t ws_bytes, void *stream) {
+// slot_map null: rows at (tok_seq, tok_pos); else rows at the slots of a paged cache.
+static dsa_status write_rows(const dsa_cache_writer *cw, const int32_t *slot_map, void *ws, size_t ws_bytes,
+                             void *stream) {
     if (!cw || cw->n_tok < 0 || cw->hidden < 64 || cw->hidden % 8 != 0) return DSA_ERR_INVALID;
-    if (!cw->h || !cw->w || !cw->rms_weight || !cw->ln_weight || !cw->ln_bias || !cw->tok_seq || !cw->tok_pos)
+    if (!cw->h || !cw->w || !cw->rms_weight || !cw->ln_weight || !cw->ln_bias || !cw->tok_pos)
         return DSA_ERR_INVALID;
+    if (!slot_map && !cw->tok_seq) return DSA_ERR_INVALID;
     if (!cw->kv && !cw->k_idx) return DSA_ERR_INVALID;
     if (cw->n_seq < 1 || cw->max_ctx < 1 || !(cw->eps > 0.f) || !(cw->rope_theta > 1.f)) return DSA_ERR_INVALID;
     if (cw->h_row_stride < cw->hidden || cw->h_row_stride % 8 != 0 || !a16(cw->h) || !a16(cw->w))
@@ -298,6 +311,7 @@ dsa_status dsa_write_cache_rows(const dsa_cache_writer *cw, void *ws, size_t ws_
     e.ln_bias = cw->ln_bias;
     e.tok_seq = cw->tok_seq;
     e.tok_pos = cw->tok_pos;
+    e.slot_map = slot_map;
     e.kv = cw->kv;
     e.kv_seq_stride = cw->kv_seq_stride;
     e.kv_row_stride = cw->kv_row_stride;
@@ -310,6 +324,18 @@ dsa_status dsa_write_cache_rows(const dsa_cache_writer *cw, void *ws, size_t ws_
     e.log2_theta = log2(static_cast<double>(cw->rope_theta));
     e.status = static_cast<uint32_t *>(ws);
     return launch_cache_write_epilogue(e, st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+dsa_status dsa_write_cache_rows(const dsa_cache_writer *cw, void *ws, size_t ws_bytes, void *stream) {
+    return write_rows(cw, nullptr, ws, ws_bytes, stream);
+}
+
+dsa_status dsa_write_paged_rows(const dsa_cache_writer *cw, const int32_t *slot_map, void *ws, size_t ws_bytes,
+                                void *stream) {
+    // n_seq pages of max_ctx rows: slots are int32
+    if (!cw || static_cast<int64_t>(cw->n_seq) * cw->max_ctx > INT32_MAX) return DSA_ERR_INVALID;
+    if (!slot_map) return cw->n_tok == 0 ? DSA_OK : DSA_ERR_INVALID;
+    return write_rows(cw, slot_map, ws, ws_bytes, stream);
 }
 
 dsa_status dsa_absorb_queries(int32_t n_q, int32_t heads, const void *q_nope, const void *q_rope, const void *w_uk_t,

@@ -543,6 +543,194 @@ dsa_status dsa_up_project(int32_t n_q, int32_t heads, const void *o_lat, const v
                           size_t ws_bytes, void *stream);
 
 /*
+ * Paged caches.  The pages name inference serving and the cache bytes per token
+ * ["GLM-5.2 -- LLM architectures explained", "Modelled costs"] but no memory
+ * manager; pages are this library's reading of how a server holds the caches of
+ * many requests.  A pool holds n_pages pages of page_rows rows; sequence b's row
+ * s is row s % page_rows of page block_table[b][s / page_rows], and its slot is
+ * page * page_rows + s % page_rows.  One step of a server:
+ *   dsa_page_tables      pages for the new tokens, their positions and slots
+ *   dsa_write_paged_rows the new tokens' cache rows
+ *   dsa_paged_mla        their attention over the pages
+ *   dsa_verify_drafts    which drafted tokens stand
+ * and the next step's dsa_page_tables with the lengths that verification left.
+ */
+
+/*
+ * Block tables and slot maps from request lengths (all pointers device memory).
+ *   n_seq, n_tok  sequences; capacity of the token arrays (>= sum of new_len)
+ *   n_pages, page_rows   the pool (n_pages * page_rows <= 2^31 - 1)
+ *   max_pages     entries of a block-table row
+ *   ctx_len       [n_seq] rows already cached
+ *   new_len       [n_seq] tokens of this step (0 allowed)
+ *   held          [n_seq] pages the sequence holds already: entries 0..held-1 of
+ *                 its row (more than ctx_len needs after rejected drafts, or
+ *                 where pages are reserved ahead)
+ *   free_pages    [n_free] page ids to hand out, from index *free_begin on
+ *                 (free_begin NULL = 0)
+ *   block_table   [n_seq] rows table_stride apart: entries held .. need-1 are
+ *                 written, need = max(held, ceil((ctx_len + new_len) / page_rows));
+ *                 the others are left as they are
+ * Outputs:
+ *   q_begin       [n_seq + 1] exclusive prefix sum of new_len
+ *   seq_len       [n_seq] ctx_len + new_len
+ *   q_seq, q_pos, slot_map  [n_tok] each token's sequence, position and slot;
+ *                 0, 0 and -1 for tokens past the last sequence's
+ *   held_out      [n_seq] need
+ *   free_used     [1] pages handed out
+ * Pages are handed out in sequence order.  The inputs are left as they are (the
+ * next step passes held_out and free_begin + free_used), so outputs must not
+ * alias inputs (DSA_ERR_INVALID for the same pointer); a repeated call gives the
+ * same result.  Token arrays may be NULL when n_tok is 0, free_pages when n_free
+ * is 0.  Device-detected errors set DSA_ERR_INVALID in the status word, and
+ * nothing out of range is written: a negative length (taken as 0), a length past
+ * the table (its entries stop at max_pages, slots past it are -1), a page id
+ * outside the pool or an exhausted free list (entry and slots -1), more tokens
+ * than n_tok (the tokens past it are dropped and q_begin stops there).
+ *   ws            at least 256 bytes (status word)
+ */
+typedef struct {
+    int32_t n_seq;
+    int32_t n_tok;
+    int32_t n_pages;
+    int32_t page_rows;
+    int32_t max_pages;
+    int32_t n_free;
+    const int32_t *ctx_len;
+    const int32_t *new_len;
+    const int32_t *held;
+    const int32_t *free_pages;
+    const int32_t *free_begin;
+    int32_t *block_table;
+    int64_t table_stride; /* elements, >= max_pages */
+    int32_t *q_begin;
+    int32_t *seq_len;
+    int32_t *q_seq;
+    int32_t *q_pos;
+    int32_t *slot_map;
+    int32_t *held_out;
+    int32_t *free_used;
+} dsa_page_plan;
+dsa_status dsa_page_tables(const dsa_page_plan *plan, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * dsa_write_cache_rows into paged caches: token i's rows go to slot_map[i]
+ * instead of (tok_seq[i], tok_pos[i]).  The writer's fields keep their meaning
+ * except
+ *   n_seq, max_ctx   pages of the pool, rows per page
+ *   kv_seq_stride, k_seq_stride   page strides (elements)
+ *   tok_seq          not read (may be NULL)
+ *   tok_pos          the RoPE position only (any value >= 0)
+ *   slot_map         device int32 [n_tok]; -1 writes nothing for that token (the
+ *                    padding of dsa_page_tables); any other slot outside the pool,
+ *                    or a negative position, skips the token and sets
+ *                    DSA_ERR_INVALID.  Two tokens must not share a slot.
+ *   ws               dsa_cache_writer_workspace_bytes(n_tok, hidden) bytes
+ */
+dsa_status dsa_write_paged_rows(const dsa_cache_writer *writer, const int32_t *slot_map, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/*
+ * The tokens of one paged attention call: sequence b's new tokens are rows
+ * q_begin[b] .. q_begin[b+1]-1 of the query, the last ones of its seq_len[b]
+ * rows (their own rows included, already written).
+ *   n_seq, n_tok   sequences; rows of the query and output arrays
+ *   block_table    device int32, rows table_stride apart, max_pages entries each
+ *   q_begin        device int32 [n_seq + 1], not decreasing, 0 <= .. <= n_tok
+ *   seq_len        device int32 [n_seq], >= the sequence's new tokens,
+ *                  <= max_pages * page_rows
+ */
+typedef struct {
+    int32_t n_seq;
+    int32_t n_tok;
+    int32_t n_pages;
+    int32_t page_rows;
+    int32_t max_pages;
+    const int32_t *block_table;
+    int64_t table_stride; /* elements, >= max_pages */
+    const int32_t *q_begin;
+    const int32_t *seq_len;
+} dsa_paged_batch;
+
+/*
+ * Absorbed MLA of new tokens over every row they see in a paged latent cache
+ * [TM, Multi-head latent attention; Learnable attention sink]: token j of
+ * sequence b (n new tokens) stands at position t = seq_len[b] - n + j and attends
+ * over rows 0..t:
+ *   l_s = scale * (q_lat . c_s + q_rope . r_s),  out = sum_s softmax(l)_s c_s,
+ *   lse = log sum_s exp(l_s).
+ * One token per sequence is decode, a base token with its drafts a few, a prompt
+ * chunk many; one call takes any mix.  (Contexts of up to topk rows need no
+ * indexer: every row is selected.)
+ *   mla   as for dsa_sparse_mla_*, with kv the pool: row r of page p at
+ *         kv + p * kv_seq_stride + r * kv_row_stride (packed FP8 rows: strides in
+ *         bytes).  Heads: 1 or more.
+ *   ws    dsa_paged_mla_workspace_bytes(batch, mla) bytes, 256-byte aligned
+ * Output rows outside [q_begin[0], q_begin[n_seq]) are left as they were.  Pool
+ * rows at or past a sequence's seq_len may hold anything, NaN included.  A token
+ * that sees no row (every page missing) gives 0 and an lse of -infinity.
+ * Device-detected errors set DSA_ERR_INVALID in the status word: a sequence whose
+ * q_begin or seq_len is out of range is skipped, a page outside the pool counts
+ * as rows nobody sees.
+ * Paths: bf16 queries with up to 128 heads x (512 + 64) over bf16 or packed FP8
+ * rows run on tcgen05 tensor cores when page_rows is a multiple of 8 and the pool
+ * is aligned as dsa_mla asks, its page stride a whole number of rows; other bf16
+ * and float32 shapes run a CUDA-core kernel.
+ */
+dsa_status dsa_paged_mla(const dsa_paged_batch *batch, const dsa_mla *mla, void *ws, size_t ws_bytes, void *stream);
+size_t dsa_paged_mla_workspace_bytes(const dsa_paged_batch *batch, const dsa_mla *mla);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given
+ * random numbers (speculative sampling; the draft tokens are those of
+ * dsa_sparse_mla_mtp's groups).  Request r drafted tokens x_0 .. x_{n-1}; p_i is
+ * the target's distribution after i of them, q_i the draft's:
+ *   x_i is accepted while accept_u[r][i] * q_i(x_i) < p_i(x_i);
+ *   at the first rejection i the next token is drawn from max(p_i - q_i, 0), and
+ *   with every draft accepted from p_n: the lowest j whose cumulative weight
+ *   exceeds sample_u[r] times the total weight.
+ * The comparison and the cumulative weights are taken in float64.
+ *   n_req, n_draft   requests; drafts per request (>= 0), the row length of
+ *                    draft_tokens and accept_u
+ *   vocab, dtype     >= 1; DSA_F32 or DSA_BF16, for target and draft
+ *   target           p: row i of request r at target + r*t_req_stride +
+ *                    i*t_row_stride (elements), n_draft + 1 rows
+ *   draft            q likewise, n_draft rows; or NULL: drafts chosen greedily,
+ *                    q_i one at x_i and zero elsewhere
+ *   draft_tokens     int32 [n_req][n_draft]
+ *   draft_len        int32 [n_req], 0..n_draft drafts of each request; NULL = all
+ *   accept_u         float32 [n_req][n_draft];  sample_u  float32 [n_req]; in [0, 1)
+ *   tokens           int32 [n_req][n_draft + 1]: the accepted drafts, the drawn
+ *                    token, then -1
+ *   n_accept         int32 [n_req]: accepted drafts
+ *   ws               at least 256 bytes (status word)
+ * Probabilities need not be normalised; values that are negative or not finite
+ * count as 0.  Where p_i <= q_i everywhere (rounding), the token is drawn from
+ * p_i.  Device-detected errors set DSA_ERR_INVALID: a draft token outside the
+ * vocabulary (rejected, nothing subtracted for it), a draft_len out of range
+ * (clamped), a distribution without weight (token -1).
+ */
+typedef struct {
+    int32_t n_req;
+    int32_t n_draft;
+    int32_t vocab;
+    int32_t dtype;
+    const void *target;
+    int64_t t_req_stride;
+    int64_t t_row_stride;
+    const void *draft;
+    int64_t d_req_stride;
+    int64_t d_row_stride;
+    const int32_t *draft_tokens;
+    const int32_t *draft_len;
+    const float *accept_u;
+    const float *sample_u;
+    int32_t *tokens;
+    int32_t *n_accept;
+} dsa_verify;
+dsa_status dsa_verify_drafts(const dsa_verify *verify, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Upper bound of the workspace bytes an operation needs (host only).
  *   op         a dsa_op value
  *   queries    n_q and max_ctx are read (pointers are not)
