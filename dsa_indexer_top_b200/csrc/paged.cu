@@ -351,6 +351,33 @@ dsa_status check_batch(const dsa_paged_batch *b) {
     return DSA_OK;
 }
 
+PagedMlaArgs paged_args(const dsa_paged_batch *batch, const dsa_mla *mla, void *ws) {
+    PagedMlaArgs a = {};
+    a.q = mla->q;
+    a.kv = mla->kv;
+    a.out = mla->out;
+    a.lse = mla->lse;
+    a.kv_page_stride = mla->kv_seq_stride;
+    a.kv_row_stride = mla->kv_row_stride;
+    a.block_table = batch->block_table;
+    a.table_stride = batch->table_stride;
+    a.q_begin = batch->q_begin;
+    a.seq_len = batch->seq_len;
+    a.n_seq = batch->n_seq;
+    a.n_tok = batch->n_tok;
+    a.n_pages = batch->n_pages;
+    a.page_rows = batch->page_rows;
+    a.max_pages = batch->max_pages;
+    a.heads = mla->heads;
+    a.d_lat = mla->d_latent;
+    a.d_rope = mla->d_rope;
+    a.scale = mla->scale;
+    a.is_bf16 = mla->dtype == DSA_BF16;
+    a.kv_fp8 = mla_kv_fp8(mla);
+    a.status = static_cast<uint32_t *>(ws);
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -383,7 +410,7 @@ dsa_status dsa_page_tables(const dsa_page_plan *p, void *ws, size_t ws_bytes, vo
 
 size_t dsa_paged_mla_workspace_bytes(const dsa_paged_batch *batch, const dsa_mla *mla) {
     if (check_batch(batch) != DSA_OK || check_mla_layers(mla, 1) != DSA_OK) return 0;
-    return kStatus;
+    return kStatus + (paged_mla_tc_shape(paged_args(batch, mla, nullptr)) ? paged_mla_tc_scratch(sm_count_current()) : 0);
 }
 
 dsa_status dsa_paged_mla(const dsa_paged_batch *batch, const dsa_mla *mla, void *ws, size_t ws_bytes, void *stream) {
@@ -399,30 +426,12 @@ dsa_status dsa_paged_mla(const dsa_paged_batch *batch, const dsa_mla *mla, void 
                 mla->kv_row_stride % 16 != 0 || mla->kv_seq_stride % 16 != 0 || !aligned16(mla->kv)))
         return DSA_ERR_UNSUPPORTED;
     if (mla->heads > 65535 || mla->d_latent + mla->d_rope > kGenMaxDims) return DSA_ERR_UNSUPPORTED;
-    PagedMlaArgs a = {};
-    a.q = mla->q;
-    a.kv = mla->kv;
-    a.out = mla->out;
-    a.lse = mla->lse;
-    a.kv_page_stride = mla->kv_seq_stride;
-    a.kv_row_stride = mla->kv_row_stride;
-    a.block_table = batch->block_table;
-    a.table_stride = batch->table_stride;
-    a.q_begin = batch->q_begin;
-    a.seq_len = batch->seq_len;
-    a.n_seq = batch->n_seq;
-    a.n_tok = batch->n_tok;
-    a.n_pages = batch->n_pages;
-    a.page_rows = batch->page_rows;
-    a.max_pages = batch->max_pages;
-    a.heads = mla->heads;
-    a.d_lat = mla->d_latent;
-    a.d_rope = mla->d_rope;
-    a.scale = mla->scale;
-    a.is_bf16 = mla->dtype == DSA_BF16;
-    a.kv_fp8 = fp8;
-    a.status = static_cast<uint32_t *>(ws);
-    return launch_paged_mla_generic(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    const PagedMlaArgs a = paged_args(batch, mla, ws);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = paged_mla_tc_shape(a) ? launch_paged_mla_tc(a, static_cast<uint8_t *>(ws) + kStatus,
+                                                                      sm_count_current(), st)
+                                                : launch_paged_mla_generic(a, st);
+    return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // extern "C"
