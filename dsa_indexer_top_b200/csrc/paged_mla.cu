@@ -33,6 +33,7 @@
 // float32 partials (O, maximum, sum) in the workspace, merged by a second kernel.
 // The ranges follow from the lengths alone, which every cluster sums for itself
 // (the units of a sequence's row tiles are a sum of floors, in closed form).
+#include <cfloat>
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -48,16 +49,20 @@ constexpr int kRows = 128;                       // rows of a row tile
 constexpr int kKeys = 128;                       // cache rows of a key tile
 constexpr int kBlk = 64 * 128;                   // 64 rows x 64 dims, bf16: 8 KB
 constexpr int kNB = kRow / 64;                   // 9 blocks of 64 dims
-constexpr int kQBytes = kNB * 2 * kBlk;          // 144 KB: the query tile
-constexpr int kKStage = 2 * kBlk;                // 128 keys x 64 dims
+constexpr int kQTmem = 7;                        // query blocks held in tensor memory
+constexpr int kQBytes = (kNB - kQTmem) * 2 * kBlk;  // the others
+constexpr int kKStage = 2 * kBlk;                // 128 keys (or query rows) x 64 dims
+constexpr int kKStages = 8;
 constexpr int kVStage = 4 * kBlk;                // 64 keys x 256 dims
-constexpr int kStages = 5;                       // of either ring
+constexpr int kVStages = 5;
 constexpr int kPSlot = 4 * kBlk;                 // 128 rows x 128 keys
-constexpr int kBig = kQBytes + kStages * kKStage;
-static_assert(kBig == 2 * kPSlot + kStages * kVStage, "both CTAs fill the same space");
+constexpr int kBig = kQBytes + 2 * kPSlot + kKStages * kKStage;
+static_assert(kBig == 2 * kPSlot + kVStages * kVStage, "both CTAs fill the same space");
 constexpr int kSmemMax = 232448;                 // 227 KB
 constexpr int kThreads = 320;                    // 8 softmax / output warps, producer, MMA
-constexpr int kSBufs = 4;
+constexpr int kSBufs = 2;
+constexpr int kQCol = kSBufs * kKeys;            // TMEM column of the query blocks, 32 columns each
+static_assert(kQCol + 32 * kQTmem <= 512, "tensor memory");
 constexpr float kRescale = 8.0f;                 // log2: P stays below 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -71,12 +76,12 @@ enum { kCmdRescale = 0, kCmdFinish = 1, kCmdExit = 2 };
 // mapped to the other rank.
 struct Small {
     // score CTA
-    uint64_t q_full, q_free, k_full[kStages], k_free[kStages], s_full[kSBufs], s_free[kSBufs];
+    uint64_t q_full, q_free, k_full[kKStages], k_free[kKStages], s_full[kSBufs], s_free[kSBufs];
     uint64_t x_bar[4];        // the two warps of a quadrant exchange their maxima
     uint64_t p_free[2];       // P V of the slot's tile has completed (from the value CTA)
     uint64_t stat_free;       // the value CTA has read the row statistics
     // value CTA
-    uint64_t p_full[2], v_full[kStages], v_free[kStages], cmd_full, cmd_done, stat_full;
+    uint64_t p_full[2], v_full[kVStages], v_free[kVStages], cmd_full, cmd_done, stat_full;
     uint64_t fin;
     uint32_t tmem_base;
     int abort;
@@ -117,19 +122,40 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_remote_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
 __device__ __forceinline__ void st_remote(uint32_t a, uint32_t x) {
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
+__device__ __forceinline__ void arrive_expect_remote(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+// Copy of own shared memory into the other CTA's, counted on a barrier there.
+__device__ __forceinline__ void copy_remote(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+// 128 rows x 32 bytes of a K-major tile into 8 TMEM columns.
+__device__ __forceinline__ void tmem_copy(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// umma_bf16 with A in tensor memory (row m in lane m, two values per column).
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 // Arrive on the barrier of the same address in the CTAs of `mask` when this
 // thread's earlier MMAs have completed.
 __device__ __forceinline__ void umma_commit_to(uint64_t *bar, uint16_t mask) {
@@ -379,14 +405,28 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
     uint32_t it = 0, tile = 0, piece = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
-        // the query tile, once the previous piece's products have read theirs
-        if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
+        // the query tile: seven blocks through the ring (the MMA thread moves them on to
+        // tensor memory), the last two into their own space once the previous piece's
+        // products have read it
         const int halves = w.rows() > 64 ? 2 : 1;
-        if (lane == 0) mbar_arrive_expect_tx(&sm->q_full, halves * kNB * kBlk);
+        const int qrow = static_cast<int>(w.row0());
+        for (int kb = 0; kb < kQTmem; ++kb, ++it) {
+            const int st = it % kKStages;
+            if (it >= kKStages && !mbar_wait(&sm->k_free[st], (it / kKStages - 1) & 1, a.p.status, &sm->abort)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[st], halves * kBlk);
+            __syncwarp();
+            if (lane < halves)
+                tma_load_2d(k_sm + st * kKStage + lane * kBlk, mq, &sm->k_full[st], 64 * kb, qrow + 64 * lane);
+        }
+        if (!ok || (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sm->q_full, halves * (kNB - kQTmem) * kBlk);
         __syncwarp();
-        if (lane < kNB * halves) {
-            const int kb = lane % kNB, hf = lane / kNB;
-            tma_load_2d(q_sm + kb * 2 * kBlk + hf * kBlk, mq, &sm->q_full, 64 * kb, static_cast<int>(w.row0()) + 64 * hf);
+        if (lane < (kNB - kQTmem) * halves) {
+            const int kb = lane >> (halves - 1), hf = lane & (halves - 1);
+            tma_load_2d(q_sm + kb * 2 * kBlk + hf * kBlk, mq, &sm->q_full, 64 * (kQTmem + kb), qrow + 64 * hf);
         }
         for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
             const int need = w.keys(kt) > 64 ? kKeys : 64;
@@ -402,8 +442,8 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
                 if (lane == 0) report_status(a.p.status, DSA_ERR_INVALID);
             }
             for (int kb = 0; kb < kNB; ++kb, ++it) {
-                const int st = it % kStages;
-                if (it >= kStages && !mbar_wait(&sm->k_free[st], (it / kStages - 1) & 1, a.p.status, &sm->abort)) {
+                const int st = it % kKStages;
+                if (it >= kKStages && !mbar_wait(&sm->k_free[st], (it / kKStages - 1) & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
@@ -426,8 +466,8 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
     }
     // every copy has landed before the CTA may exit
     __syncwarp();
-    for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-        mbar_wait(&sm->k_full[i % kStages], (i / kStages) & 1, a.p.status, nullptr);
+    for (uint32_t i = it > kKStages ? it - kKStages : 0; i < it; ++i)
+        mbar_wait(&sm->k_full[i % kKStages], (i / kKStages) & 1, a.p.status, nullptr);
     if (piece > 0) mbar_wait(&sm->q_full, (piece - 1) & 1, a.p.status, nullptr);
 }
 
@@ -438,7 +478,21 @@ __device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *k_
     uint32_t it = 0, tile = 0, piece = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
-        if (!mbar_wait(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
+        // query blocks to tensor memory, after the previous piece's products
+        if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
+        for (int kb = 0; kb < kQTmem; ++kb, ++it) {
+            const int st = it % kKStages;
+            if (!mbar_wait(&sm->k_full[st], (it / kKStages) & 1, a.p.status, &sm->abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tmem_copy(tb + kQCol + 32 * kb + 8 * k, kd + static_cast<uint64_t>((st * kKStage + k * 32) >> 4));
+            umma_commit(&sm->k_free[st]);
+        }
+        if (!ok || !mbar_wait(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
         for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
             const uint32_t buf = tile % kSBufs;
             const uint32_t idesc = w.keys(kt) > 64 ? kIdescS128 : kIdescS64;
@@ -447,16 +501,22 @@ __device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *k_
                 break;
             }
             for (int kb = 0; kb < kNB; ++kb, ++it) {
-                const int st = it % kStages;
-                if (!mbar_wait(&sm->k_full[st], (it / kStages) & 1, a.p.status, &sm->abort)) {
+                const int st = it % kKStages;
+                if (!mbar_wait(&sm->k_full[st], (it / kKStages) & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                const uint64_t bd = kd + static_cast<uint64_t>((st * kKStage) >> 4);
+                if (kb < kQTmem) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_bf16(tb + kKeys * buf, qd + ((kb * 2 * kBlk + k * 32) >> 4),
-                              kd + static_cast<uint64_t>((st * kKStage + k * 32) >> 4), idesc, kb + k > 0 ? 1u : 0u);
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16_ta(tb + kKeys * buf, tb + kQCol + 32 * kb + 8 * k, bd + 2 * k, idesc, kb + k > 0 ? 1u : 0u);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(tb + kKeys * buf, qd + (((kb - kQTmem) * 2 * kBlk + k * 32) >> 4), bd + 2 * k, idesc, 1u);
+                }
                 umma_commit(&sm->k_free[st]);
             }
             if (ok) umma_commit(&sm->s_full[buf]);
@@ -468,7 +528,7 @@ __device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *k_
 }
 
 // Warp w: rows 32 (w & 3) + lane, keys 64 (w >> 2) .. + 63 of every tile.
-__device__ void score_softmax(const TcArgs &a, Small *sm, uint32_t p_remote) {
+__device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint32_t p_remote) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
     const int r = 32 * quad + lane;
     const uint32_t tb = sm->tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + 64 * half;
@@ -507,8 +567,6 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint32_t p_remote) {
             float mx = -INFINITY;
             if (live && used) {
                 const int s0 = kt * kKeys + 64 * half;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) x[i] = __float_as_uint(u2f(x[i]) * c2);
                 if (s0 + 63 > pos0 || okbits != 0xFFFFu) {
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
@@ -516,6 +574,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint32_t p_remote) {
                 }
 #pragma unroll
                 for (int i = 0; i < 64; ++i) mx = fmaxf(mx, u2f(x[i]));
+                mx *= c2;  // (scale > 0)
             }
             float al = 1.f;
             if (live) {
@@ -543,29 +602,40 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint32_t p_remote) {
             }
             if (live) {
                 const float mu = m == -INFINITY ? 0.f : m;
-                const uint32_t pr = p_remote + slot * kPSlot + half * 2 * kBlk;
+                uint8_t *pl = p_stage + slot * kPSlot + half * 2 * kBlk;
+                if (used) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float p[8];
+                    for (int c = 0; c < 8; ++c) {
+                        float p[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        p[i] = used ? ex2(u2f(x[8 * c + i]) - mu) : 0.f;
-                        l += p[i];
+                        for (int i = 0; i < 8; ++i) {
+                            p[i] = ex2(fmaf(u2f(x[8 * c + i]), c2, -mu));
+                            l += p[i];
+                        }
+                        // bf16 weights for the MMA; the sum keeps the float32 values, so the
+                        // roundings (half a step, 2^-8 relative) average out in the output
+                        *reinterpret_cast<uint4 *>(pl + sw128_offset(r, c)) =
+                            make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
+                                       pack_bf16(p[6], p[7]));
                     }
-                    // bf16 weights for the MMA; the sum keeps the float32 values, so the
-                    // roundings (half a step, 2^-8 relative) average out in the output
-                    if (used)
-                        st_remote_v4(pr + sw128_offset(r, c), pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
-                                     pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
                 }
             }
             if (half == 0) {
-                if (flag) st_remote(r_alpha + (slot * kRows + r) * 4, __float_as_uint(al));
+                if (flag) {
+                    st_remote(r_alpha + (slot * kRows + r) * 4, __float_as_uint(al));
+                    fence_cluster();
+                }
                 if (lane == 0) st_remote(r_flags + (slot * 4 + quad) * 4, flag ? 1u : 0u);
             }
-            fence_proxy_async_all();  // P is read by the other CTA's tensor cores
+            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_remote(r_pfull + slot * 8);
+            if (lane == 0) {
+                // the warp's 32 rows x 64 keys are 4 KB in a row of the staged tile
+                const uint32_t off = slot * kPSlot + half * 2 * kBlk + quad * 4096;
+                const bool send = live && used;
+                arrive_expect_remote(r_pfull + slot * 8, send ? 4096 : 0);
+                if (send) copy_remote(p_remote + off, smem_u32(p_stage) + off, 4096, r_pfull + slot * 8);
+            }
         }
         if (!ok) break;
         // row statistics to the value CTA: both halves' sums joined
@@ -609,8 +679,8 @@ __device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const 
             int row = a.oob_row;
             if (lane < 2 * boxes) row = box_row(a, w, kt * kKeys + lane * a.box, missing);
             for (int g = 0; g < 2 * khs; ++g, ++it) {
-                const int d = g / khs, kh = g % khs, st = it % kStages;  // dims 256 d .., keys 64 kh ..
-                if (it >= kStages && !mbar_wait(&sm->v_free[st], (it / kStages - 1) & 1, a.p.status, &sm->abort)) {
+                const int d = g / khs, kh = g % khs, st = it % kVStages;  // dims 256 d .., keys 64 kh ..
+                if (it >= kVStages && !mbar_wait(&sm->v_free[st], (it / kVStages - 1) & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
@@ -626,8 +696,8 @@ __device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const 
         }
     }
     __syncwarp();
-    for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-        mbar_wait(&sm->v_full[i % kStages], (i / kStages) & 1, a.p.status, nullptr);
+    for (uint32_t i = it > kVStages ? it - kVStages : 0; i < it; ++i)
+        mbar_wait(&sm->v_full[i % kVStages], (i / kVStages) & 1, a.p.status, nullptr);
 }
 
 // Posts a command to the output warps; they start once this thread's MMAs have
@@ -656,7 +726,6 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
                 ok = false;
                 break;
             }
-            fence_proxy_async_all();
             tc_fence_after();
             const volatile int *fl = sm->flags[slot];
             if (fl[0] | fl[1] | fl[2] | fl[3]) {
@@ -671,8 +740,8 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
                 tc_fence_after();
             }
             for (int g = 0; g < 2 * khs; ++g, ++it) {
-                const int d = g / khs, kh = g % khs, st = it % kStages;
-                if (!mbar_wait(&sm->v_full[st], (it / kStages) & 1, a.p.status, &sm->abort)) {
+                const int d = g / khs, kh = g % khs, st = it % kVStages;
+                if (!mbar_wait(&sm->v_full[st], (it / kVStages) & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
@@ -811,9 +880,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         mbar_init(&sm->q_full, 1);
         mbar_init(&sm->q_free, 1);
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kKStages; ++i) {
             mbar_init(&sm->k_full[i], 1);
             mbar_init(&sm->k_free[i], 1);
+        }
+        for (int i = 0; i < kVStages; ++i) {
             mbar_init(&sm->v_full[i], 1);
             mbar_init(&sm->v_free[i], 1);
         }
@@ -851,11 +922,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync_all();  // both CTAs' barriers are set up before either signals the other
     if (rank == 0) {
         if (warp < 8)
-            score_softmax(a, sm, map_rank(smem_u32(smem), 1));
+            score_softmax(a, sm, smem + kQBytes, map_rank(smem_u32(smem), 1));
         else if (warp == 8)
-            score_producer(a, sm, smem, smem + kQBytes, &mq, &mkv);
+            score_producer(a, sm, smem, smem + kQBytes + 2 * kPSlot, &mq, &mkv);
         else if (lane == 0)
-            score_mma(a, sm, smem, smem + kQBytes);
+            score_mma(a, sm, smem, smem + kQBytes + 2 * kPSlot);
     } else {
         if (warp < 8)
             value_output(a, sm, cluster);
@@ -917,7 +988,8 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 
 bool paged_mla_tc_shape(const PagedMlaArgs &a) {
-    if (!a.is_bf16 || a.kv_fp8 || a.heads > kRows || a.d_lat != kLatent || a.d_rope != kRope) return false;
+    // (the softmax takes the maximum before it scales: a positive scale)
+    if (!a.is_bf16 || a.kv_fp8 || !(a.scale > 0.f) || a.scale > FLT_MAX || a.heads > kRows || a.d_lat != kLatent || a.d_rope != kRope) return false;
     if (a.page_rows % 8 != 0 || a.kv_row_stride % 8 != 0 || a.kv_row_stride < kRow) return false;
     if (a.kv_page_stride % a.kv_row_stride != 0) return false;
     const int64_t pitch = a.kv_page_stride / a.kv_row_stride;
