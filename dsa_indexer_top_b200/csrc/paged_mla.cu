@@ -49,10 +49,11 @@ constexpr int kRows = 128;                       // rows of a row tile
 constexpr int kKeys = 128;                       // cache rows of a key tile
 constexpr int kBlk = 64 * 128;                   // 64 rows x 64 dims, bf16: 8 KB
 constexpr int kNB = kRow / 64;                   // 9 blocks of 64 dims
-constexpr int kQTmem = 7;                        // query blocks held in tensor memory
-constexpr int kQBytes = (kNB - kQTmem) * 2 * kBlk;  // the others
-constexpr int kKStage = 2 * kBlk;                // 128 keys (or query rows) x 64 dims
-constexpr int kKStages = 8;
+constexpr int kQTmem = 8;                        // query blocks held in tensor memory (the latent ones)
+constexpr int kQBytes = (kNB - kQTmem) * 2 * kBlk;  // the RoPE block, in shared memory
+constexpr int kKBlocks = 3;                      // 64-dim blocks per stage
+constexpr int kKStage = kKBlocks * 2 * kBlk;     // 128 keys (or query rows) x 192 dims
+constexpr int kKStages = kNB / kKBlocks;
 constexpr int kVStage = 4 * kBlk;                // 64 keys x 256 dims
 constexpr int kVStages = 5;
 constexpr int kPSlot = 4 * kBlk;                 // 128 rows x 128 keys
@@ -66,8 +67,7 @@ static_assert(kQCol + 32 * kQTmem <= 512, "tensor memory");
 constexpr float kRescale = 8.0f;                 // log2: P stays below 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint32_t kIdescS128 = idesc_bf16(128, 128, false, false);
-constexpr uint32_t kIdescS64 = idesc_bf16(128, 64, false, false);
+constexpr uint32_t kIdescS = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(128, 256, false, true);
 
 enum { kCmdRescale = 0, kCmdFinish = 1, kCmdExit = 2 };
@@ -77,9 +77,11 @@ enum { kCmdRescale = 0, kCmdFinish = 1, kCmdExit = 2 };
 struct Small {
     // score CTA
     uint64_t q_full, q_free, k_full[kKStages], k_free[kKStages], s_full[kSBufs], s_free[kSBufs];
-    uint64_t x_bar[4];        // the two warps of a quadrant exchange their maxima
+    uint64_t m_bar[2][4];     // [tile parity][quadrant]: the tile's running maxima are in m_run
+    uint64_t l_bar[4];        // the odd tiles' sums are in
+    uint64_t l_read[4];       // .. and have been read: both groups leave a piece together
     uint64_t p_free[2];       // P V of the slot's tile has completed (from the value CTA)
-    uint64_t stat_free;       // the value CTA has read the row statistics
+    uint64_t out_done;        // the value CTA has written a piece's result (its P slots are free)
     // value CTA
     uint64_t p_full[2], v_full[kVStages], v_free[kVStages], cmd_full, cmd_done, stat_full;
     uint64_t fin;
@@ -91,7 +93,9 @@ struct Small {
     int flags[2][4];          // value CTA: [slot][quadrant] some row's O must be rescaled
     uint32_t key_ok[kSBufs];  // score CTA: [S buffer] bit i: keys 8i..8i+7 are in the pool
     union {
-        float xmax[2][2][kRows];  // score CTA: [parity][half][row]
+        struct {
+            float m_run[kRows], m_odd[kRows], l_odd[kRows];  // score CTA
+        } q;
         struct {
             float alpha[2][kRows];  // value CTA: [slot][row]
             float m[kRows], l[kRows];
@@ -108,9 +112,7 @@ struct TcArgs {
     PagedMlaArgs p;
     int clusters;
     int tok_tile;       // tokens per row tile
-    int page_pitch;     // rows from one page to the next in the pool's row space
-    int box;            // rows per TMA box (divides page_rows, 8..64)
-    int oob_row;        // a row coordinate past the pool: TMA fills zeros
+    int box;            // rows per TMA copy (divides page_rows, 8..64)
     Meta *meta;         // [clusters]
     float *part_ml;     // [2 * clusters][128][2] maximum (log2), sum
     float *part_o;      // [2 * clusters][128][512]
@@ -122,11 +124,15 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_remote(uint32_t a, uint32_t x) {
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+// A store to the other CTA's shared memory, counted (4 bytes) on a barrier there.
+__device__ __forceinline__ void st_remote(uint32_t a, uint32_t x, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(a), "r"(x), "r"(bar)
+                 : "memory");
 }
+// (relaxed: what the barrier announces comes by copies and stores that it counts
+// itself; a release at cluster scope waits 2000 cycles for earlier stores)
 __device__ __forceinline__ void arrive_expect_remote(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
 // Copy of own shared memory into the other CTA's, counted on a barrier there.
@@ -150,9 +156,8 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -383,57 +388,85 @@ struct Walk {
     __device__ int keys(int kt) const { return min(kKeys, seen() - kt * kKeys); }
 };
 
-// Row coordinate, in the pool's row space, of the cache rows s..s+box-1 (one page
-// holds them); past the sequence or outside the pool: a coordinate that fills zeros.
-__device__ __forceinline__ int box_row(const TcArgs &a, const Walk &w, int s, bool &missing) {
-    missing = false;
-    if (s >= w.s.len) return a.oob_row;
+// The page of cache rows s..s+box-1 (one page holds them) as a TMA coordinate, and
+// their 8-row group in it; past the sequence or outside the pool: page n_pages, for
+// which TMA fills zeros.
+struct Box {
+    int page, group;
+    bool missing;
+};
+__device__ __forceinline__ Box find_box(const TcArgs &a, const Walk &w, int s) {
+    Box x = {a.p.n_pages, 0, false};
+    if (s >= w.s.len) return x;
     const int pi = s / a.p.page_rows;
     const int page = __ldg(a.p.block_table + w.b * a.p.table_stride + pi);
     if (page < 0 || page >= a.p.n_pages) {
-        missing = true;
-        return a.oob_row;
+        x.missing = true;
+        return x;
     }
-    return page * a.page_pitch + (s - pi * a.p.page_rows);
+    x.page = page;
+    x.group = (s - pi * a.p.page_rows) >> 3;
+    return x;
+}
+
+// Copies of cache rows land as [8-row group][64-dim block][8 rows][128 bytes], a
+// swizzle atom per (group, block): a run of blocks of a whole page comes with one
+// instruction (each costs the issuing thread some 80 cycles), and both products'
+// descriptors take the strides between groups and blocks.
+__device__ __forceinline__ void tma_load_rows(void *dst, const CUtensorMap *map, uint64_t *bar, int block, const Box &x) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(0), "r"(block), "r"(x.group), "r"(x.page)
+        : "memory");
 }
 
 // ------------------------------------------------------------------ score CTA
+// Stage i of the ring holds blocks 3i..3i+2 of the key tiles, and of the query tile
+// before them: constant addresses let the MMA thread issue at full rate.
 __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *k_sm, const CUtensorMap *mq,
-                               const CUtensorMap *mkv) {
+                               const CUtensorMap *mk) {
     const int lane = threadIdx.x & 31;
-    const int boxes = kKeys / a.box;  // per block, 2..16: one lane each
-    uint32_t it = 0, tile = 0, piece = 0;
+    const int boxes = kKeys / a.box;  // per stage, 2..16: one lane each
+    uint32_t fills = 0, tile = 0, q_use = 0;  // fills of each stage so far
     bool ok = true;
+    auto stage_free = [&](int i) {
+        return fills == 0 || mbar_wait(&sm->k_free[i], (fills - 1) & 1, a.p.status, &sm->abort);
+    };
+    uint32_t piece = 0, part = 0;  // part: stages filled of the current round
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
-        // the query tile: seven blocks through the ring (the MMA thread moves them on to
-        // tensor memory), the last two into their own space once the previous piece's
-        // products have read it
+        Box x = {a.p.n_pages, 0, false};
+        if (lane < boxes) x = find_box(a, w, w.k0 * kKeys + lane * a.box);
+        // the query tile: the latent blocks through the ring (the MMA thread moves them on
+        // to tensor memory), the RoPE block into its own space
         const int halves = w.rows() > 64 ? 2 : 1;
         const int qrow = static_cast<int>(w.row0());
-        for (int kb = 0; kb < kQTmem; ++kb, ++it) {
-            const int st = it % kKStages;
-            if (it >= kKStages && !mbar_wait(&sm->k_free[st], (it / kKStages - 1) & 1, a.p.status, &sm->abort)) {
+        for (int i = 0; ok && i < kKStages; ++i) {
+            const int nb = i < kKStages - 1 ? kKBlocks : kQTmem - kKBlocks * (kKStages - 1);
+            if (!stage_free(i)) {
                 ok = false;
                 break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[st], halves * kBlk);
+            part = i + 1;
+            if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[i], halves * nb * kBlk);
             __syncwarp();
-            if (lane < halves)
-                tma_load_2d(k_sm + st * kKStage + lane * kBlk, mq, &sm->k_full[st], 64 * kb, qrow + 64 * lane);
+            if (lane < nb * halves) {
+                const int kb = lane >> (halves - 1), hf = lane & (halves - 1);
+                tma_load_2d(k_sm + i * kKStage + kb * 2 * kBlk + hf * kBlk, mq, &sm->k_full[i], 64 * (kKBlocks * i + kb),
+                            qrow + 64 * hf);
+            }
         }
-        if (!ok || (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sm->q_full, halves * (kNB - kQTmem) * kBlk);
+        if (!ok) break;
+        ++fills;
+        part = 0;
+        if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
+        ++q_use;
+        if (lane == 0) mbar_arrive_expect_tx(&sm->q_full, halves * kBlk);
         __syncwarp();
-        if (lane < (kNB - kQTmem) * halves) {
-            const int kb = lane >> (halves - 1), hf = lane & (halves - 1);
-            tma_load_2d(q_sm + kb * 2 * kBlk + hf * kBlk, mq, &sm->q_full, 64 * (kQTmem + kb), qrow + 64 * hf);
-        }
+        if (lane < halves) tma_load_2d(q_sm + lane * kBlk, mq, &sm->q_full, 64 * kQTmem, qrow + 64 * lane);
         for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
             const int need = w.keys(kt) > 64 ? kKeys : 64;
-            bool missing = false;
-            int row = a.oob_row;
-            if (lane < boxes) row = box_row(a, w, kt * kKeys + lane * a.box, missing);
-            const unsigned miss = __ballot_sync(0xffffffffu, missing);
+            const unsigned miss = __ballot_sync(0xffffffffu, x.missing);
             uint32_t okbits = 0xFFFFu;
             if (miss) {
                 okbits = 0;
@@ -441,85 +474,105 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
                     if (!((miss >> (i * 8 / a.box)) & 1)) okbits |= 1u << i;
                 if (lane == 0) report_status(a.p.status, DSA_ERR_INVALID);
             }
-            for (int kb = 0; kb < kNB; ++kb, ++it) {
-                const int st = it % kKStages;
-                if (it >= kKStages && !mbar_wait(&sm->k_free[st], (it / kKStages - 1) & 1, a.p.status, &sm->abort)) {
+            // key_ok of this tile's S buffer: its previous tile has been read
+            if (tile >= kSBufs && !mbar_wait(&sm->s_free[tile % kSBufs], (tile / kSBufs - 1) & 1, a.p.status, &sm->abort)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) sm->key_ok[tile % kSBufs] = okbits;
+            for (int i = 0; i < kKStages; ++i) {
+                if (!stage_free(i)) {
                     ok = false;
                     break;
                 }
-                if (kb == 0) {
-                    // (the S buffer of this tile is free: its s_free came before the MMA of the
-                    // tile four back could be overtaken; checked here for key_ok's sake)
-                    if (tile >= kSBufs &&
-                        !mbar_wait(&sm->s_free[tile % kSBufs], (tile / kSBufs - 1) & 1, a.p.status, &sm->abort)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) sm->key_ok[tile % kSBufs] = okbits;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[st], need * 128);
+                part = i + 1;
+                if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[i], need * kKBlocks * 128);
                 __syncwarp();
                 if (lane * a.box < need)
-                    tma_load_2d(k_sm + st * kKStage + lane * a.box * 128, mkv, &sm->k_full[st], 64 * kb, row);
+                    tma_load_rows(k_sm + i * kKStage + lane * a.box * kKBlocks * 128, mk, &sm->k_full[i], kKBlocks * i, x);
             }
+            if (!ok) break;
+            ++fills;
+            part = 0;
+            // the next tile's pages are looked up while this one's copies run
+            if (kt + 1 < w.k1 && lane < boxes) x = find_box(a, w, (kt + 1) * kKeys + lane * a.box);
         }
     }
     // every copy has landed before the CTA may exit
     __syncwarp();
-    for (uint32_t i = it > kKStages ? it - kKStages : 0; i < it; ++i)
-        mbar_wait(&sm->k_full[i % kKStages], (i / kKStages) & 1, a.p.status, nullptr);
-    if (piece > 0) mbar_wait(&sm->q_full, (piece - 1) & 1, a.p.status, nullptr);
+    for (uint32_t i = 0; i < kKStages; ++i) {
+        const uint32_t n = fills + (i < part ? 1 : 0);
+        if (n > 0) mbar_wait(&sm->k_full[i], (n - 1) & 1, a.p.status, nullptr);
+    }
+    if (q_use > 0) mbar_wait(&sm->q_full, (q_use - 1) & 1, a.p.status, nullptr);
+}
+
+// One unit's 36 MMAs into S buffer kBuf.  Tensor memory is allocated whole, so its
+// base is 0 and every address and descriptor here is a constant: an operand that
+// has to be moved to a uniform register first costs the issuing thread more than
+// the 64 cycles an MMA takes (measured: 115 cycles per MMA with a computed stage).
+// A tile of 64 keys or fewer multiplies what an earlier tile left in the upper
+// half too; those columns are not read.
+template <int kBuf>
+__device__ __forceinline__ bool score_tile(const TcArgs &a, Small *sm, uint32_t q_addr, uint32_t k_addr, uint32_t parity) {
+#pragma unroll
+    for (int i = 0; i < kKStages; ++i) {
+        if (!mbar_wait(&sm->k_full[i], parity, a.p.status, &sm->abort)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < kKBlocks; ++j) {
+            const int kb = i * kKBlocks + j;
+            const uint64_t bd = sdesc_sw128(k_addr + i * kKStage + j * 1024, 16, kKBlocks * 1024);
+            if (kb < kQTmem) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_bf16_ta(kKeys * kBuf, kQCol + 32 * kb + 8 * k, bd + 2 * k, kIdescS, kb + k > 0 ? 1u : 0u);
+            } else {
+                const uint64_t ad = sdesc_sw128(q_addr, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_bf16(kKeys * kBuf, ad + 2 * k, bd + 2 * k, kIdescS, 1u);
+            }
+        }
+        umma_commit(&sm->k_free[i]);
+    }
+    umma_commit(&sm->s_full[kBuf]);
+    return true;
 }
 
 __device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *k_sm) {
-    const uint32_t tb = sm->tmem_base;
-    const uint64_t qd = sdesc_sw128(smem_u32(q_sm), 16, 1024);
-    const uint64_t kd = sdesc_sw128(smem_u32(k_sm), 16, 1024);
-    uint32_t it = 0, tile = 0, piece = 0;
+    const uint32_t q_addr = smem_u32(q_sm), k_addr = smem_u32(k_sm);
+    uint32_t tile = 0, piece = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
         // query blocks to tensor memory, after the previous piece's products
         if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
-        for (int kb = 0; kb < kQTmem; ++kb, ++it) {
-            const int st = it % kKStages;
-            if (!mbar_wait(&sm->k_full[st], (it / kKStages) & 1, a.p.status, &sm->abort)) {
+#pragma unroll
+        for (int i = 0; i < kKStages; ++i) {
+            if (!ok || !mbar_wait(&sm->k_full[i], (tile + piece) & 1, a.p.status, &sm->abort)) {
                 ok = false;
-                break;
+                continue;
             }
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                tmem_copy(tb + kQCol + 32 * kb + 8 * k, kd + static_cast<uint64_t>((st * kKStage + k * 32) >> 4));
-            umma_commit(&sm->k_free[st]);
+            for (int j = 0; j < kKBlocks; ++j) {
+                const int kb = i * kKBlocks + j;
+                if (kb >= kQTmem) continue;
+                const uint64_t kd = sdesc_sw128(k_addr + i * kKStage + j * 2 * kBlk, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_copy(kQCol + 32 * kb + 8 * k, kd + 2 * k);
+            }
+            umma_commit(&sm->k_free[i]);
         }
         if (!ok || !mbar_wait(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
         for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
             const uint32_t buf = tile % kSBufs;
-            const uint32_t idesc = w.keys(kt) > 64 ? kIdescS128 : kIdescS64;
             if (tile >= kSBufs && !mbar_wait(&sm->s_free[buf], (tile / kSBufs - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
-            for (int kb = 0; kb < kNB; ++kb, ++it) {
-                const int st = it % kKStages;
-                if (!mbar_wait(&sm->k_full[st], (it / kKStages) & 1, a.p.status, &sm->abort)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t bd = kd + static_cast<uint64_t>((st * kKStage) >> 4);
-                if (kb < kQTmem) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_bf16_ta(tb + kKeys * buf, tb + kQCol + 32 * kb + 8 * k, bd + 2 * k, idesc, kb + k > 0 ? 1u : 0u);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_bf16(tb + kKeys * buf, qd + (((kb - kQTmem) * 2 * kBlk + k * 32) >> 4), bd + 2 * k, idesc, 1u);
-                }
-                umma_commit(&sm->k_free[st]);
-            }
-            if (ok) umma_commit(&sm->s_full[buf]);
+            tc_fence_after();
+            const uint32_t par = (tile + piece + 1) & 1;
+            ok = buf ? score_tile<1>(a, sm, q_addr, k_addr, par) : score_tile<0>(a, sm, q_addr, k_addr, par);
         }
         if (ok) umma_commit(&sm->q_free);
     }
@@ -527,16 +580,20 @@ __device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *k_
     mbar_wait(&sm->fin, 0, a.p.status, nullptr);
 }
 
-// Warp w: rows 32 (w & 3) + lane, keys 64 (w >> 2) .. + 63 of every tile.
+// Softmax.  Warps 0-3 take the even tiles, 4-7 the odd ones, so that one tile's
+// exponentials run beside the next one's loads and exchanges; thread r of a group
+// holds row r's 128 logits.  The running maxima pass from tile to tile through
+// shared memory; each group keeps the sum of its own tiles, relative to the maximum
+// it saw last.
 __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint32_t p_remote) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, group = warp >> 2;
     const int r = 32 * quad + lane;
-    const uint32_t tb = sm->tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + 64 * half;
+    const uint32_t tb = static_cast<uint32_t>(32 * quad) << 16;
     const float c2 = a.p.scale * kLog2e;
     const uint32_t r_alpha = map_rank(smem_u32(&sm->v.alpha[0][0]), 1), r_flags = map_rank(smem_u32(&sm->flags[0][0]), 1);
     const uint32_t r_pfull = map_rank(smem_u32(&sm->p_full[0]), 1), r_stat = map_rank(smem_u32(&sm->stat_full), 1);
     const uint32_t r_m = map_rank(smem_u32(&sm->v.m[0]), 1), r_l = map_rank(smem_u32(&sm->v.l[0]), 1);
-    uint32_t tile = 0, piece = 0, xphase = 0;
+    uint32_t tile = 0, piece = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
         const int rows = w.rows();
@@ -547,69 +604,83 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         const int pos0 = w.s.len - w.s.n + w.rt * a.tok_tile;  // the tile's first token
         float m = -INFINITY, l = 0.f;
         for (int kt = w.k0; kt < w.k1; ++kt, ++tile) {
-            const uint32_t buf = tile % kSBufs, slot = tile & 1;
-            if (!mbar_wait(&sm->s_full[buf], (tile / kSBufs) & 1, a.p.status, &sm->abort)) {
+            const uint32_t slot = tile & 1;  // of P, and of the S buffers
+            if (slot != static_cast<uint32_t>(group)) continue;
+            if (!mbar_wait(&sm->s_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const uint32_t okbits = *reinterpret_cast<volatile uint32_t *>(&sm->key_ok[buf]);
-            const bool used = 64 * half < w.keys(kt);  // (with up to 64 keys the upper half was not computed)
-            uint32_t x[64];
-            if (live && used) {
-                tmem_ld32(tb + kKeys * buf, reinterpret_cast<uint32_t(&)[32]>(x[0]));
-                tmem_ld32(tb + kKeys * buf + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
+            const uint32_t okbits = *reinterpret_cast<volatile uint32_t *>(&sm->key_ok[slot]);
+            const int nk = w.keys(kt);
+            uint32_t x[128];
+            if (live) {
+#pragma unroll
+                for (int c = 0; c < 128; c += 32)
+                    tmem_ld32(tb + kKeys * slot + c, reinterpret_cast<uint32_t(&)[32]>(x[c]));
                 tmem_ld_wait();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->s_free[buf]);
+            if (lane == 0) mbar_arrive(&sm->s_free[slot]);
             float mx = -INFINITY;
-            if (live && used) {
-                const int s0 = kt * kKeys + 64 * half;
-                if (s0 + 63 > pos0 || okbits != 0xFFFFu) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (s0 + i > pos || !((okbits >> (8 * half + i / 8)) & 1)) x[i] = 0xFF800000u;
-                }
-#pragma unroll
-                for (int i = 0; i < 64; ++i) mx = fmaxf(mx, u2f(x[i]));
-                mx *= c2;  // (scale > 0)
-            }
-            float al = 1.f;
             if (live) {
-                sm->xmax[tile & 1][half][r] = mx;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
-                if (!mbar_wait(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) {
+                const int s0 = kt * kKeys;
+                if (s0 + kKeys - 1 > pos0 || okbits != 0xFFFFu) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (s0 + i > pos || !((okbits >> (i / 8)) & 1)) x[i] = 0xFF800000u;
+                }
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 128; i += 4)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], u2f(x[i + k]));
+                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;  // (scale > 0)
+            }
+            // the previous tile's running maximum
+            float mp = -INFINITY;
+            if (kt > w.k0) {
+                if (!mbar_wait(&sm->m_bar[slot ^ 1][quad], ((tile - 1) >> 1) & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
-                xphase ^= 1;
-                mx = fmaxf(mx, sm->xmax[tile & 1][half ^ 1][r]);
-                if (m == -INFINITY) {
-                    m = mx;  // nothing accumulated for the row yet
-                } else if (r < rows && mx > m + kRescale) {
-                    al = ex2(m - mx);
-                    m = mx;
-                    l *= al;
-                }
+                mp = sm->q.m_run[r];
             }
+            float mn = mp, al = 1.f;
+            if (mp == -INFINITY) {
+                mn = mx;  // nothing accumulated for the row yet
+            } else if (r < rows && mx > mp + kRescale) {
+                al = ex2(mp - mx);
+                mn = mx;
+            }
+            sm->q.m_run[r] = mn;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->m_bar[slot][quad]);
+            if (m != -INFINITY && m != mn) l *= ex2(m - mn);
+            m = mn;
             const bool flag = __any_sync(0xffffffffu, al != 1.f);
+            // (the value CTA stages a piece's result in the P slots)
+            if (kt < w.k0 + 2 && piece > 0 && !mbar_wait_cluster(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) {
+                ok = false;
+                break;
+            }
             if (tile >= 2 && !mbar_wait_cluster(&sm->p_free[slot], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
             if (live) {
                 const float mu = m == -INFINITY ? 0.f : m;
-                uint8_t *pl = p_stage + slot * kPSlot + half * 2 * kBlk;
-                if (used) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (hf && nk <= 64) break;
+                    uint8_t *pl = p_stage + slot * kPSlot + hf * 2 * kBlk;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         float p[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            p[i] = ex2(fmaf(u2f(x[8 * c + i]), c2, -mu));
+                            p[i] = ex2(fmaf(u2f(x[64 * hf + 8 * c + i]), c2, -mu));
                             l += p[i];
                         }
                         // bf16 weights for the MMA; the sum keeps the float32 values, so the
@@ -620,64 +691,59 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                     }
                 }
             }
-            if (half == 0) {
-                if (flag) {
-                    st_remote(r_alpha + (slot * kRows + r) * 4, __float_as_uint(al));
-                    fence_cluster();
-                }
-                if (lane == 0) st_remote(r_flags + (slot * 4 + quad) * 4, flag ? 1u : 0u);
-            }
+            if (flag) st_remote(r_alpha + (slot * kRows + r) * 4, __float_as_uint(al), r_pfull + slot * 8);
+            if (lane == 0) st_remote(r_flags + (slot * 4 + quad) * 4, flag ? 1u : 0u, r_pfull + slot * 8);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 // the warp's 32 rows x 64 keys are 4 KB in a row of the staged tile
-                const uint32_t off = slot * kPSlot + half * 2 * kBlk + quad * 4096;
-                const bool send = live && used;
-                arrive_expect_remote(r_pfull + slot * 8, send ? 4096 : 0);
-                if (send) copy_remote(p_remote + off, smem_u32(p_stage) + off, 4096, r_pfull + slot * 8);
+                const uint32_t off = slot * kPSlot + quad * 4096;
+                const int parts = !live ? 0 : nk > 64 ? 2 : 1;
+                arrive_expect_remote(r_pfull + slot * 8, parts * 4096 + (flag ? 132 : 4));
+                for (int hf = 0; hf < parts; ++hf)
+                    copy_remote(p_remote + off + hf * 2 * kBlk, smem_u32(p_stage) + off + hf * 2 * kBlk, 4096,
+                                r_pfull + slot * 8);
             }
         }
         if (!ok) break;
-        // row statistics to the value CTA: both halves' sums joined
-        if (piece > 0 && !mbar_wait_cluster(&sm->stat_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
-        if (live) {
-            // (every read of this parity's maxima is past: the other parity's barrier followed)
-            sm->xmax[tile & 1][half][r] = l;
+        // row statistics to the value CTA, the odd tiles' sum joined to the even tiles'
+        // (a piece's result is out before the next piece's first P: see out_done)
+        if (group == 1) {
+            sm->q.m_odd[r] = m;
+            sm->q.l_odd[r] = l;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
-            if (!mbar_wait(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
-            xphase ^= 1;
-            if (half == 0) {
-                l += sm->xmax[tile & 1][1][r];
-                st_remote(r_m + r * 4, __float_as_uint(m));
-                st_remote(r_l + r * 4, __float_as_uint(l));
+            if (lane == 0) mbar_arrive(&sm->l_bar[quad]);
+            if (!mbar_wait(&sm->l_read[quad], piece & 1, a.p.status, &sm->abort)) break;
+        } else {
+            if (!mbar_wait(&sm->l_bar[quad], piece & 1, a.p.status, &sm->abort)) break;
+            const float mo = sm->q.m_odd[r], lo = sm->q.l_odd[r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->l_read[quad]);
+            const float mf = fmaxf(m, mo);  // (the later tile's: running maxima do not fall)
+            if (mf != -INFINITY) l = l * ex2(m - mf) + lo * ex2(mo - mf);
+            if (piece > 0 && !mbar_wait_cluster(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) break;
+            if (live) {
+                st_remote(r_m + r * 4, __float_as_uint(mf), r_stat);
+                st_remote(r_l + r * 4, __float_as_uint(l), r_stat);
             }
-            // the partner has read before the next tile writes this parity again
-            if (half == 0) __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
-            if (!mbar_wait(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
-            xphase ^= 1;
-        }
-        if (half == 0) {
             __syncwarp();
-            if (lane == 0) arrive_remote(r_stat);
+            if (lane == 0) arrive_expect_remote(r_stat, live ? 256 : 0);
         }
     }
 }
 
 // ------------------------------------------------------------------ value CTA
-__device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const CUtensorMap *mkv) {
+__device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const CUtensorMap *mv) {
     const int lane = threadIdx.x & 31;
-    const int boxes = 64 / a.box;  // of 64 rows x 64 dims, 1..8
+    const int boxes = 64 / a.box;  // per stage, 1..8: one lane each
     uint32_t it = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next()) {
+        // lane i looks up box i of the tile's 128 rows, a tile ahead
+        Box x = {a.p.n_pages, 0, false};
+        if (lane < 2 * boxes) x = find_box(a, w, w.k0 * kKeys + lane * a.box);
         for (int kt = w.k0; ok && kt < w.k1; ++kt) {
             const int khs = w.keys(kt) > 64 ? 2 : 1;
-            // lane i looks up box i of the tile
-            bool missing = false;
-            int row = a.oob_row;
-            if (lane < 2 * boxes) row = box_row(a, w, kt * kKeys + lane * a.box, missing);
             for (int g = 0; g < 2 * khs; ++g, ++it) {
                 const int d = g / khs, kh = g % khs, st = it % kVStages;  // dims 256 d .., keys 64 kh ..
                 if (it >= kVStages && !mbar_wait(&sm->v_free[st], (it / kVStages - 1) & 1, a.p.status, &sm->abort)) {
@@ -686,13 +752,11 @@ __device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const 
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&sm->v_full[st], kVStage);
                 __syncwarp();
-                // 4 dim blocks x boxes, one per lane (4..32)
-                const int bx = lane >> 2, db = lane & 3;
-                const int y = __shfl_sync(0xffffffffu, row, kh * boxes + min(bx, boxes - 1));
-                if (bx < boxes)
-                    tma_load_2d(v_sm + st * kVStage + db * kBlk + bx * a.box * 128, mkv, &sm->v_full[st], 256 * d + 64 * db,
-                                y);
+                const int i = lane - kh * boxes;
+                if (i >= 0 && i < boxes)
+                    tma_load_rows(v_sm + st * kVStage + i * a.box * 4 * 128, mv, &sm->v_full[st], 4 * d, x);
             }
+            if (kt + 1 < w.k1 && lane < 2 * boxes) x = find_box(a, w, (kt + 1) * kKeys + lane * a.box);
         }
     }
     __syncwarp();
@@ -715,7 +779,7 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
     const int lane = threadIdx.x & 31;
     const uint32_t tb = sm->tmem_base;
     const uint64_t pd = sdesc_sw128(smem_u32(p_sm), 16, 1024);
-    const uint64_t vd = sdesc_sw128(smem_u32(v_sm), kBlk, 1024);
+    const uint64_t vd = sdesc_sw128(smem_u32(v_sm), 1024, 4096);
     uint32_t it = 0, tile = 0, cphase = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next()) {
@@ -749,9 +813,10 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
                 const int z0 = w.s.len - kt * kKeys - 64 * kh;
                 if (z0 < 64) {
                     uint8_t *v = v_sm + st * kVStage;
-                    for (int i = lane; i < 4 * (64 - z0) * 8; i += 32) {
-                        const int db = i & 3, rest = i >> 2;
-                        *reinterpret_cast<uint4 *>(v + db * kBlk + z0 * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
+                    for (int i = lane; i < 32 * (64 - z0); i += 32) {
+                        const int row = z0 + (i >> 5), db = (i >> 3) & 3;
+                        *reinterpret_cast<uint4 *>(v + (row >> 3) * 4096 + db * 1024 + (row & 7) * 128 + (i & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -761,7 +826,7 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         umma_bf16(tb + 256 * d, pd + static_cast<uint64_t>((slot * kPSlot + kh * 2 * kBlk + k * 32) >> 4),
-                                  vd + static_cast<uint64_t>((st * kVStage + k * 2048) >> 4), kIdescO,
+                                  vd + static_cast<uint64_t>((st * kVStage + k * 8192) >> 4), kIdescO,
                                   (kt > w.k0 || kh + k > 0) ? 1u : 0u);
                     umma_commit(&sm->v_free[st]);
                 }
@@ -786,11 +851,11 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
 }
 
 // Warp w: rows 32 (w & 3) + lane, output dims 256 (w >> 2) .. + 255.
-__device__ void value_output(const TcArgs &a, Small *sm, int cluster) {
+__device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, int cluster) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
     const int r = 32 * quad + lane;
     const uint32_t tb = sm->tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + 256 * half;
-    const uint32_t r_free = map_rank(smem_u32(&sm->stat_free), 0);
+    const uint32_t r_done = map_rank(smem_u32(&sm->out_done), 0);
     uint32_t cphase = 0, piece = 0;
     Walk w(a, sm);
     while (true) {
@@ -824,27 +889,57 @@ __device__ void value_output(const TcArgs &a, Small *sm, int cluster) {
             const int64_t row = w.row0() + r;
             const int64_t pslot = 2 * cluster + (w.k0 == 0 ? 1 : 0);
             if (32 * quad < rows) {
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.p.out) + row * kLatent + 256 * half;
-                float *po = a.part_o + (pslot * kRows + r) * kLatent + 256 * half;
+                // 64 columns at a time through the warp's 8 KB of the P slots (16-byte pieces
+                // exchanged by row, so that neither side conflicts), then whole rows to memory:
+                // a lane's own 16-byte stores, 2 KB apart, took four times as long
+                uint8_t *st = stage + warp * 8192;
+                const int n_live = min(32, rows - 32 * quad);
+                const int64_t row_w = row - lane;  // the warp's first row
+                if (whole) {
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
-                    uint32_t x[32];
-                    tmem_ld32(tb + c, x);
-                    tmem_ld_wait();
-                    if (live && whole) {
+                    for (int c = 0; c < 256; c += 128) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            *reinterpret_cast<uint4 *>(o + c + i) =
-                                make_uint4(pack_bf16(u2f(x[i]) * inv, u2f(x[i + 1]) * inv),
-                                           pack_bf16(u2f(x[i + 2]) * inv, u2f(x[i + 3]) * inv),
-                                           pack_bf16(u2f(x[i + 4]) * inv, u2f(x[i + 5]) * inv),
-                                           pack_bf16(u2f(x[i + 6]) * inv, u2f(x[i + 7]) * inv));
-                    } else if (live) {
+                        for (int g = 0; g < 4; ++g) {
+                            uint32_t x[32];
+                            tmem_ld32(tb + c + 32 * g, x);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4 *>(po + c + i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                            for (int i = 0; i < 32; i += 8)
+                                *reinterpret_cast<uint4 *>(st + lane * 256 + (((4 * g + i / 8) ^ (lane & 15)) << 4)) =
+                                    make_uint4(pack_bf16(u2f(x[i]) * inv, u2f(x[i + 1]) * inv),
+                                               pack_bf16(u2f(x[i + 2]) * inv, u2f(x[i + 3]) * inv),
+                                               pack_bf16(u2f(x[i + 4]) * inv, u2f(x[i + 5]) * inv),
+                                               pack_bf16(u2f(x[i + 6]) * inv, u2f(x[i + 7]) * inv));
+                        }
+                        __syncwarp();
+                        uint8_t *o = static_cast<uint8_t *>(a.p.out) + (row_w * kLatent + 256 * half + c) * 2;
+                        for (int i = lane >> 4; i < n_live; i += 2)
+                            *reinterpret_cast<uint4 *>(o + static_cast<int64_t>(i) * kLatent * 2 + (lane & 15) * 16) =
+                                *reinterpret_cast<const uint4 *>(st + i * 256 + (((lane & 15) ^ (i & 15)) << 4));
+                        __syncwarp();
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 256; c += 64) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t x[32];
+                            tmem_ld32(tb + c + 32 * g, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<uint4 *>(st + lane * 256 + (((8 * g + i / 4) ^ (lane & 15)) << 4)) =
+                                    make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        }
+                        __syncwarp();
+                        float *po = a.part_o + (pslot * kRows + 32 * quad) * kLatent + 256 * half + c;
+                        for (int i = lane >> 4; i < n_live; i += 2)
+                            *reinterpret_cast<uint4 *>(po + i * kLatent + (lane & 15) * 4) =
+                                *reinterpret_cast<const uint4 *>(st + i * 256 + (((lane & 15) ^ (i & 15)) << 4));
+                        __syncwarp();
                     }
                 }
+                fence_proxy_async_smem();  // (the slots are next written by a copy)
             }
             if (live && half == 0) {
                 if (!whole) {
@@ -861,7 +956,7 @@ __device__ void value_output(const TcArgs &a, Small *sm, int cluster) {
                 a.meta[cluster] = Meta{end - cluster + 1, static_cast<int>(w.row0()), rows, 0};
             }
             __syncwarp();
-            if (lane == 0) arrive_remote(r_free);
+            if (lane == 0) arrive_remote(r_done);
             ++piece;
             w.next();
         }
@@ -872,7 +967,8 @@ __device__ void value_output(const TcArgs &a, Small *sm, int cluster) {
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    paged_mla_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv) {
+    paged_mla_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                        const __grid_constant__ CUtensorMap mv) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Small *sm = reinterpret_cast<Small *>(smem + kBig);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -890,14 +986,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kSBufs; ++i) {
             mbar_init(&sm->s_full[i], 1);
-            mbar_init(&sm->s_free[i], 8);
+            mbar_init(&sm->s_free[i], 4);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&sm->x_bar[i], 2);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sm->m_bar[0][i], 1);
+            mbar_init(&sm->m_bar[1][i], 1);
+            mbar_init(&sm->l_bar[i], 1);
+            mbar_init(&sm->l_read[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm->p_free[i], 1);
-            mbar_init(&sm->p_full[i], 8);
+            mbar_init(&sm->p_full[i], 4);
         }
-        mbar_init(&sm->stat_free, 8);
+        mbar_init(&sm->out_done, 8);
         mbar_init(&sm->stat_full, 4);
         mbar_init(&sm->cmd_full, 2);
         mbar_init(&sm->cmd_done, 8);
@@ -911,11 +1012,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (warp == 8 && lane == 0) {
         tma_prefetch_desc(&mq);
-        tma_prefetch_desc(&mkv);
+        tma_prefetch_desc(&mk);
+        tma_prefetch_desc(&mv);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && sm->tmem_base != 0) {  // (the whole of it: its base is 0)
+        report_status(a.p.status, DSA_ERR_CUDA);
+        sm->abort = 1;
+    }
     griddep_wait();
     make_plan(a, sm, cluster, rank == 0 && cluster == 0);
     if (tid == 0 && rank == 1) a.meta[cluster].parts = 0;
@@ -924,14 +1030,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (warp < 8)
             score_softmax(a, sm, smem + kQBytes, map_rank(smem_u32(smem), 1));
         else if (warp == 8)
-            score_producer(a, sm, smem, smem + kQBytes + 2 * kPSlot, &mq, &mkv);
+            score_producer(a, sm, smem, smem + kQBytes + 2 * kPSlot, &mq, &mk);
         else if (lane == 0)
             score_mma(a, sm, smem, smem + kQBytes + 2 * kPSlot);
     } else {
         if (warp < 8)
-            value_output(a, sm, cluster);
+            value_output(a, sm, smem, cluster);
         else if (warp == 8)
-            value_producer(a, sm, smem + 2 * kPSlot, &mkv);
+            value_producer(a, sm, smem + 2 * kPSlot, &mv);
         else
             value_mma(a, sm, smem, smem + 2 * kPSlot);
     }
@@ -991,11 +1097,9 @@ bool paged_mla_tc_shape(const PagedMlaArgs &a) {
     // (the softmax takes the maximum before it scales: a positive scale)
     if (!a.is_bf16 || a.kv_fp8 || !(a.scale > 0.f) || a.scale > FLT_MAX || a.heads > kRows || a.d_lat != kLatent || a.d_rope != kRope) return false;
     if (a.page_rows % 8 != 0 || a.kv_row_stride % 8 != 0 || a.kv_row_stride < kRow) return false;
-    if (a.kv_page_stride % a.kv_row_stride != 0) return false;
-    const int64_t pitch = a.kv_page_stride / a.kv_row_stride;
+    if (a.kv_page_stride % 8 != 0 || a.kv_page_stride < 1) return false;
     const auto mis = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.kv) | reinterpret_cast<uintptr_t>(a.out);
-    return (mis & 15u) == 0 && (a.n_pages - 1) * pitch + a.page_rows < INT32_MAX &&
-           static_cast<int64_t>(a.n_tok) * a.heads < INT32_MAX;
+    return (mis & 15u) == 0 && static_cast<int64_t>(a.n_tok) * a.heads < INT32_MAX;
 }
 
 size_t paged_mla_tc_scratch(int num_sms) {
@@ -1010,18 +1114,15 @@ cudaError_t launch_paged_mla_tc(const PagedMlaArgs &p, void *scratch, int num_sm
     a.p = p;
     a.clusters = num_sms / 2;
     a.tok_tile = kRows / p.heads;
-    a.page_pitch = static_cast<int>(p.kv_page_stride / p.kv_row_stride);
     a.box = 64;
     while (p.page_rows % a.box != 0) a.box >>= 1;
-    const int64_t rows = static_cast<int64_t>(p.n_pages - 1) * a.page_pitch + p.page_rows;
-    a.oob_row = static_cast<int>(rows);
     uint8_t *s = static_cast<uint8_t *>(scratch);
     a.meta = reinterpret_cast<Meta *>(s);
     s += align256(a.clusters * sizeof(Meta));
     a.part_ml = reinterpret_cast<float *>(s);
     s += align256(static_cast<size_t>(2) * a.clusters * kRows * 2 * sizeof(float));
     a.part_o = reinterpret_cast<float *>(s);
-    CUtensorMap mq, mkv;
+    CUtensorMap mq, mk, mv;
     const cuuint32_t es[2] = {1, 1};
     const cuuint64_t qd[2] = {static_cast<cuuint64_t>(kRow), static_cast<cuuint64_t>(p.n_tok) * p.heads};
     const cuuint64_t qs[1] = {static_cast<cuuint64_t>(kRow) * 2};
@@ -1030,16 +1131,21 @@ cudaError_t launch_paged_mla_tc(const PagedMlaArgs &p, void *scratch, int num_sm
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const cuuint64_t kd[2] = {static_cast<cuuint64_t>(kRow), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t ks[1] = {static_cast<cuuint64_t>(p.kv_row_stride) * 2};
-    const cuuint32_t kb[2] = {64, static_cast<cuuint32_t>(a.box)};
-    if (enc(&mkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p.kv), kd, ks, kb, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
+    // cache rows: {64 dims, 8 rows, 9 blocks, groups of a page, pages}
+    const cuuint32_t es5[5] = {1, 1, 1, 1, 1};
+    const cuuint64_t kd[5] = {64, 8, kNB, static_cast<cuuint64_t>(p.page_rows / 8), static_cast<cuuint64_t>(p.n_pages)};
+    const cuuint64_t rs = static_cast<cuuint64_t>(p.kv_row_stride) * 2;
+    const cuuint64_t ks[4] = {rs, 128, 8 * rs, static_cast<cuuint64_t>(p.kv_page_stride) * 2};
+    const cuuint32_t kb[5] = {64, 8, kKBlocks, static_cast<cuuint32_t>(a.box / 8), 1};
+    const cuuint32_t vb[5] = {64, 8, 4, static_cast<cuuint32_t>(a.box / 8), 1};
+    for (int i = 0; i < 2; ++i)
+        if (enc(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(p.kv), kd, ks, i ? vb : kb, es5,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
     cudaError_t e = set_max_dynamic_smem(paged_mla_tc_kernel, kBig + static_cast<int>(sizeof(Small)));
     if (e != cudaSuccess) return e;
-    e = launch_pdl(paged_mla_tc_kernel, dim3(2 * a.clusters), dim3(kThreads), kBig + sizeof(Small), st, a, mq, mkv);
+    e = launch_pdl(paged_mla_tc_kernel, dim3(2 * a.clusters), dim3(kThreads), kBig + sizeof(Small), st, a, mq, mk, mv);
     if (e != cudaSuccess) return e;
     return launch_pdl(paged_mla_merge_kernel, dim3(a.clusters, kRows / kMergeRows), dim3(256), 0, st, a);
 }
