@@ -23,7 +23,7 @@
 //   value CTA (rank 1)  streams value blocks (64 rows x 256 dims, 32 KB) through
 //            a ring of five and accumulates O += P V (N = 256) in all 512 TMEM
 //            columns; its eight other warps rescale O when the score CTA raised a
-//            row's maximum by more than 2^8 (rare), and write the result.
+//            row's reference maximum (rare), and write the result.
 // Both products have full-rate shapes: 36 x 64 cycles for S and 16 x 128 for O per
 // unit, so the pair is bound by the score CTA at 94% of the two SMs' peak.
 //
@@ -60,11 +60,14 @@ constexpr int kPSlot = 4 * kBlk;                 // 128 rows x 128 keys
 constexpr int kBig = kQBytes + 2 * kPSlot + kKStages * kKStage;
 static_assert(kBig == 2 * kPSlot + kVStages * kVStage, "both CTAs fill the same space");
 constexpr int kSmemMax = 232448;                 // 227 KB
-constexpr int kThreads = 320;                    // 8 softmax / output warps, producer, MMA
+constexpr int kThreads = 384;                    // 8 softmax / output warps; producer, MMA, 2 idle
 constexpr int kSBufs = 2;
 constexpr int kQCol = kSBufs * kKeys;            // TMEM column of the query blocks, 32 columns each
 static_assert(kQCol + 32 * kQTmem <= 512, "tensor memory");
-constexpr float kRescale = 8.0f;                 // log2: P stays below 2^8
+// A row's reference maximum is raised only when it grew by more than 2^32 (each time
+// costs the pair a stop): weights below 2^32 over 2^20 rows stay far inside float32
+// and bf16, whose precision does not depend on the scale.
+constexpr float kRescale = 32.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kIdescS = idesc_bf16(128, 128, false, false);
@@ -81,6 +84,7 @@ struct Small {
     uint64_t l_bar[4];        // the odd tiles' sums are in
     uint64_t l_read[4];       // .. and have been read: both groups leave a piece together
     uint64_t p_free[2];       // P V of the slot's tile has completed (from the value CTA)
+    uint64_t p_got[2];        // the slot's tile has arrived there
     uint64_t out_done;        // the value CTA has written a piece's result (its P slots are free)
     // value CTA
     uint64_t p_full[2], v_full[kVStages], v_free[kVStages], cmd_full, cmd_done, stat_full;
@@ -660,17 +664,14 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             if (m != -INFINITY && m != mn) l *= ex2(m - mn);
             m = mn;
             const bool flag = __any_sync(0xffffffffu, al != 1.f);
-            // (the value CTA stages a piece's result in the P slots)
-            if (kt < w.k0 + 2 && piece > 0 && !mbar_wait_cluster(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) {
-                ok = false;
-                break;
-            }
-            if (tile >= 2 && !mbar_wait_cluster(&sm->p_free[slot], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) {
+            // the staged tile two back has left
+            if (tile >= 2 && !mbar_wait_cluster(&sm->p_got[slot], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
             if (live) {
                 const float mu = m == -INFINITY ? 0.f : m;
+                float l4[4] = {l, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     if (hf && nk <= 64) break;
@@ -681,7 +682,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             p[i] = ex2(fmaf(u2f(x[64 * hf + 8 * c + i]), c2, -mu));
-                            l += p[i];
+                            l4[i & 3] += p[i];
                         }
                         // bf16 weights for the MMA; the sum keeps the float32 values, so the
                         // roundings (half a step, 2^-8 relative) average out in the output
@@ -690,10 +691,20 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                                        pack_bf16(p[6], p[7]));
                     }
                 }
+                l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            }
+            fence_proxy_async_smem();
+            // (the value CTA stages a piece's result in the P slots)
+            if (kt < w.k0 + 2 && piece > 0 && !mbar_wait_cluster(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) {
+                ok = false;
+                break;
+            }
+            if (tile >= 2 && !mbar_wait_cluster(&sm->p_free[slot], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) {
+                ok = false;
+                break;
             }
             if (flag) st_remote(r_alpha + (slot * kRows + r) * 4, __float_as_uint(al), r_pfull + slot * 8);
             if (lane == 0) st_remote(r_flags + (slot * 4 + quad) * 4, flag ? 1u : 0u, r_pfull + slot * 8);
-            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 // the warp's 32 rows x 64 keys are 4 KB in a row of the staged tile
@@ -790,6 +801,7 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
                 ok = false;
                 break;
             }
+            if (lane == 0) arrive_remote(map_rank(smem_u32(&sm->p_got[slot]), 0));
             tc_fence_after();
             const volatile int *fl = sm->flags[slot];
             if (fl[0] | fl[1] | fl[2] | fl[3]) {
@@ -996,6 +1008,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm->p_free[i], 1);
+            mbar_init(&sm->p_got[i], 1);
             mbar_init(&sm->p_full[i], 4);
         }
         mbar_init(&sm->out_done, 8);
@@ -1026,19 +1039,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     make_plan(a, sm, cluster, rank == 0 && cluster == 0);
     if (tid == 0 && rank == 1) a.meta[cluster].parts = 0;
     cluster_sync_all();  // both CTAs' barriers are set up before either signals the other
+    // registers from the producer's and MMA thread's warps to the others (168 each at
+    // launch: 2 x 200 + 96 of 3 x 168)
+    if (warp < 8)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (rank == 0) {
         if (warp < 8)
             score_softmax(a, sm, smem + kQBytes, map_rank(smem_u32(smem), 1));
         else if (warp == 8)
             score_producer(a, sm, smem, smem + kQBytes + 2 * kPSlot, &mq, &mk);
-        else if (lane == 0)
+        else if (warp == 9 && lane == 0)
             score_mma(a, sm, smem, smem + kQBytes + 2 * kPSlot);
     } else {
         if (warp < 8)
             value_output(a, sm, smem, cluster);
         else if (warp == 8)
             value_producer(a, sm, smem + 2 * kPSlot, &mv);
-        else
+        else if (warp == 9)
             value_mma(a, sm, smem, smem + 2 * kPSlot);
     }
     __syncwarp();
