@@ -33,6 +33,7 @@
 // float32 partials (O, maximum, sum) in the workspace, merged by a second kernel.
 // The ranges follow from the lengths alone, which every cluster sums for itself
 // (the units of a sequence's row tiles are a sum of floors, in closed form).
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 
@@ -75,6 +76,14 @@ constexpr uint32_t kIdescO = idesc_bf16(128, 256, false, true);
 
 enum { kCmdRescale = 0, kCmdFinish = 1, kCmdExit = 2 };
 
+struct Seq {  // one sequence's new tokens, rows, first query row, row tiles
+    int n, len, q0, tiles;
+};
+struct Box {  // a TMA copy of cache rows: page and 8-row group in it
+    int page, group;
+    bool missing;
+};
+
 // Same layout in both CTAs of a cluster: remote addresses are a CTA's own ones,
 // mapped to the other rank.
 struct Small {
@@ -92,6 +101,8 @@ struct Small {
     uint32_t tmem_base;
     int abort;
     int plan_b, plan_rt, plan_k0, plan_active;
+    Seq plan_seq;
+    Box plan_box[16];         // of the first key tile
     long long plan_units, plan_end, plan_total, plan_sum[kThreads / 32];
     int cmd;
     int flags[2][4];          // value CTA: [slot][quadrant] some row's O must be rescaled
@@ -213,10 +224,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ------------------------------------------------------------------ the units of a sequence
-struct Seq {
-    int n, len, q0, tiles;
-};
-
 __device__ __forceinline__ Seq make_seq(const TcArgs &a, int q0, int q1, int len, bool &bad) {
     Seq s;
     s.q0 = q0;
@@ -238,22 +245,29 @@ __device__ __forceinline__ int tile_keys(const Seq &s, int tt, int rt) {
     return (tile_seen(s, tt, rt) + kKeys - 1) / kKeys;
 }
 
-// sum_{i < n} floor((a i + b) / m), in O(log m) steps (a, b >= 0).
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
-    long long r = 0;
-    while (n > 0) {
-        r += n * (n - 1) / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const long long y = a * n + b;
-        if (y < m) break;
+// sum_{i < n} floor((a i + b) / 128), in O(log 128) steps (a <= 128, n < 2^24: a n
+// stays in 32 bits).
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+    long long r = static_cast<long long>(n) * (b >> 7);
+    b &= 127;
+    uint32_t m = 128;
+    while (true) {
+        if (a >= m) {
+            r += static_cast<long long>(n) * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            r += static_cast<long long>(n) * (b / m);
+            b %= m;
+        }
+        const uint32_t y = a * n + b;
+        if (y < m) return r;
         n = y / m;
         b = y % m;
-        const long long t = a;
+        const uint32_t t = a;
         a = m;
         m = t;
     }
-    return r;
 }
 
 // Units of the sequence's first x row tiles.  The units of tile i < tiles - 1 are
@@ -261,9 +275,26 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
 __device__ __forceinline__ long long units_before(const Seq &s, int tt, int x) {
     if (x <= 0 || s.tiles == 0) return 0;
     const int full = min(x, s.tiles - 1);
-    long long r = full > 0 ? floor_sum(full, kKeys, tt, static_cast<long long>(s.len) - s.n + tt + kKeys - 1) : 0;
+    long long r = full > 0 ? floor_sum(full, tt, static_cast<uint32_t>(s.len - s.n) + tt + kKeys - 1) : 0;
     if (x >= s.tiles) r += (s.len + kKeys - 1) / kKeys;
     return r;
+}
+
+// The page of cache rows s..s+box-1 (one page holds them) as a TMA coordinate, and
+// their 8-row group in it; past the sequence or outside the pool: page n_pages, for
+// which TMA fills zeros.
+__device__ __forceinline__ Box find_box(const TcArgs &a, const Seq &q, int b, int s) {
+    Box x = {a.p.n_pages, 0, false};
+    if (s >= q.len) return x;
+    const int pi = s / a.p.page_rows;
+    const int page = __ldg(a.p.block_table + b * a.p.table_stride + pi);
+    if (page < 0 || page >= a.p.n_pages) {
+        x.missing = true;
+        return x;
+    }
+    x.page = page;
+    x.group = (s - pi * a.p.page_rows) >> 3;
+    return x;
 }
 
 // This cluster's range of units, by all threads of the CTA: each sums the units of
@@ -317,17 +348,8 @@ __device__ void make_plan(const TcArgs &a, Small *sm, int cluster, bool report) 
             const Seq s = make_seq(a, q, q1, a.p.seq_len[b], bad);
             const long long u = units_before(s, a.tok_tile, s.tiles);
             if (start < at + u) {
-                int lo = 0, hi = s.tiles;  // last row tile whose first unit is not past the start
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (at + units_before(s, a.tok_tile, mid) <= start)
-                        lo = mid;
-                    else
-                        hi = mid;
-                }
                 sm->plan_b = b;
-                sm->plan_rt = lo;
-                sm->plan_k0 = static_cast<int>(start - at - units_before(s, a.tok_tile, lo));
+                sm->plan_sum[0] = start - at;  // unit of the sequence
                 break;
             }
             at += u;
@@ -335,6 +357,35 @@ __device__ void make_plan(const TcArgs &a, Small *sm, int cluster, bool report) 
         }
     }
     __syncthreads();
+    // the last row tile whose first unit is not past it: every thread tries one of
+    // kThreads places, twice for long chunks
+    if (sm->plan_units > 0) {
+        const int b = sm->plan_b;
+        const long long unit = sm->plan_sum[0];
+        const Seq s = make_seq(a, a.p.q_begin[b], a.p.q_begin[b + 1], a.p.seq_len[b], bad);
+        int lo = 0, span = s.tiles;  // the tile is in lo .. lo + span - 1
+        if (tid == 0) sm->plan_rt = 0;
+        while (true) {
+            const int step = (span + kThreads - 1) / kThreads;
+            const int x = lo + tid * step;
+            __syncthreads();
+            if (tid * step < span) {
+                const long long u0 = units_before(s, a.tok_tile, x);
+                const long long u1 = units_before(s, a.tok_tile, min(x + step, lo + span));
+                if (u0 <= unit && unit < u1) {
+                    sm->plan_rt = x;
+                    sm->plan_k0 = static_cast<int>(unit - u0);
+                }
+            }
+            __syncthreads();
+            if (step == 1) break;  // (uniform)
+            span = min(step, lo + span - sm->plan_rt);
+            lo = sm->plan_rt;
+        }
+        // what every role reads first: looked up here, before the copies load the memory
+        if (tid == 0) sm->plan_seq = s;
+        if (tid < kKeys / a.box) sm->plan_box[tid] = find_box(a, s, b, sm->plan_k0 * kKeys + tid * a.box);
+    }
 }
 
 // Every role walks the cluster's range by itself: piece after piece, a piece being
@@ -350,8 +401,7 @@ struct Walk {
         b = sm->plan_b;
         rt = sm->plan_rt;
         k0 = sm->plan_k0;
-        bool bad = false;
-        s = make_seq(a, a.p.q_begin[b], a.p.q_begin[b + 1], a.p.seq_len[b], bad);
+        s = sm->plan_seq;
         prefetch();
         piece();
     }
@@ -392,27 +442,6 @@ struct Walk {
     __device__ int keys(int kt) const { return min(kKeys, seen() - kt * kKeys); }
 };
 
-// The page of cache rows s..s+box-1 (one page holds them) as a TMA coordinate, and
-// their 8-row group in it; past the sequence or outside the pool: page n_pages, for
-// which TMA fills zeros.
-struct Box {
-    int page, group;
-    bool missing;
-};
-__device__ __forceinline__ Box find_box(const TcArgs &a, const Walk &w, int s) {
-    Box x = {a.p.n_pages, 0, false};
-    if (s >= w.s.len) return x;
-    const int pi = s / a.p.page_rows;
-    const int page = __ldg(a.p.block_table + w.b * a.p.table_stride + pi);
-    if (page < 0 || page >= a.p.n_pages) {
-        x.missing = true;
-        return x;
-    }
-    x.page = page;
-    x.group = (s - pi * a.p.page_rows) >> 3;
-    return x;
-}
-
 // Copies of cache rows land as [8-row group][64-dim block][8 rows][128 bytes], a
 // swizzle atom per (group, block): a run of blocks of a whole page comes with one
 // instruction (each costs the issuing thread some 80 cycles), and both products'
@@ -428,7 +457,7 @@ __device__ __forceinline__ void tma_load_rows(void *dst, const CUtensorMap *map,
 // ------------------------------------------------------------------ score CTA
 // Stage i of the ring holds blocks 3i..3i+2 of the key tiles, and of the query tile
 // before them: constant addresses let the MMA thread issue at full rate.
-__device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *k_sm, const CUtensorMap *mq,
+__device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *p_stage, uint8_t *k_sm, const CUtensorMap *mq,
                                const CUtensorMap *mk) {
     const int lane = threadIdx.x & 31;
     const int boxes = kKeys / a.box;  // per stage, 2..16: one lane each
@@ -440,34 +469,47 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
     uint32_t piece = 0, part = 0;  // part: stages filled of the current round
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
         Box x = {a.p.n_pages, 0, false};
-        if (lane < boxes) x = find_box(a, w, w.k0 * kKeys + lane * a.box);
-        // the query tile: the latent blocks through the ring (the MMA thread moves them on
-        // to tensor memory), the RoPE block into its own space
-        const int halves = w.rows() > 64 ? 2 : 1;
+        if (lane < boxes) x = piece == 0 ? sm->plan_box[lane] : find_box(a, w.s, w.b, w.k0 * kKeys + lane * a.box);
+        const bool small = w.rows() <= 64;
         const int qrow = static_cast<int>(w.row0());
-        for (int i = 0; ok && i < kKStages; ++i) {
-            const int nb = i < kKStages - 1 ? kKBlocks : kQTmem - kKBlocks * (kKStages - 1);
-            if (!stage_free(i)) {
-                ok = false;
-                break;
+        // More than 64 rows: the latent blocks of the query tile come through the ring, and
+        // the MMA thread moves them on to tensor memory; up to 64 rows they fit the space
+        // where P is staged, and the key blocks need not wait for them.
+        if (!small) {
+            for (int i = 0; ok && i < kKStages; ++i) {
+                const int nb = i < kKStages - 1 ? kKBlocks : kQTmem - kKBlocks * (kKStages - 1);
+                if (!stage_free(i)) {
+                    ok = false;
+                    break;
+                }
+                part = i + 1;
+                if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[i], 2 * nb * kBlk);
+                __syncwarp();
+                if (lane < nb * 2)
+                    tma_load_2d(k_sm + i * kKStage + lane * kBlk, mq, &sm->k_full[i], 64 * (kKBlocks * i + (lane >> 1)),
+                                qrow + 64 * (lane & 1));
             }
-            part = i + 1;
-            if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[i], halves * nb * kBlk);
-            __syncwarp();
-            if (lane < nb * halves) {
-                const int kb = lane >> (halves - 1), hf = lane & (halves - 1);
-                tma_load_2d(k_sm + i * kKStage + kb * 2 * kBlk + hf * kBlk, mq, &sm->k_full[i], 64 * (kKBlocks * i + kb),
-                            qrow + 64 * hf);
-            }
+            if (!ok) break;
+            ++fills;
+            part = 0;
         }
-        if (!ok) break;
-        ++fills;
-        part = 0;
-        if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
-        ++q_use;
-        if (lane == 0) mbar_arrive_expect_tx(&sm->q_full, halves * kBlk);
-        __syncwarp();
-        if (lane < halves) tma_load_2d(q_sm + lane * kBlk, mq, &sm->q_full, 64 * kQTmem, qrow + 64 * lane);
+        auto load_query = [&]() {
+            if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) return false;
+            if (small)  // the staged P of the last two tiles has left
+                for (uint32_t t = tile > 2 ? tile - 2 : 0; t < tile; ++t)
+                    if (!mbar_wait_cluster(&sm->p_got[t & 1], (t >> 1) & 1, a.p.status, &sm->abort)) return false;
+            ++q_use;
+            if (lane == 0) mbar_arrive_expect_tx(&sm->q_full, (small ? kNB : 2) * kBlk);
+            __syncwarp();
+            if (small) {
+                if (lane < kNB)
+                    tma_load_2d(lane < kQTmem ? p_stage + lane * kBlk : q_sm, mq, &sm->q_full, 64 * lane, qrow);
+            } else if (lane < 2) {
+                tma_load_2d(q_sm + lane * kBlk, mq, &sm->q_full, 64 * kQTmem, qrow + 64 * lane);
+            }
+            return true;
+        };
+        if (piece == 0 || !small) ok = load_query();
         for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
             const int need = w.keys(kt) > 64 ? kKeys : 64;
             const unsigned miss = __ballot_sync(0xffffffffu, x.missing);
@@ -498,8 +540,13 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
             if (!ok) break;
             ++fills;
             part = 0;
+            // (a later piece's first key blocks are on their way before its query tile)
+            if (kt == w.k0 && piece > 0 && small && !load_query()) {
+                ok = false;
+                break;
+            }
             // the next tile's pages are looked up while this one's copies run
-            if (kt + 1 < w.k1 && lane < boxes) x = find_box(a, w, (kt + 1) * kKeys + lane * a.box);
+            if (kt + 1 < w.k1 && lane < boxes) x = find_box(a, w.s, w.b, (kt + 1) * kKeys + lane * a.box);
         }
     }
     // every copy has landed before the CTA may exit
@@ -543,40 +590,52 @@ __device__ __forceinline__ bool score_tile(const TcArgs &a, Small *sm, uint32_t 
     return true;
 }
 
-__device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *k_sm) {
-    const uint32_t q_addr = smem_u32(q_sm), k_addr = smem_u32(k_sm);
-    uint32_t tile = 0, piece = 0;
+__device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *p_stage, uint8_t *k_sm) {
+    const uint32_t q_addr = smem_u32(q_sm), k_addr = smem_u32(k_sm), p_addr = smem_u32(p_stage);
+    uint32_t tile = 0, piece = 0, fills = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
         // query blocks to tensor memory, after the previous piece's products
         if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
+        if (w.rows() > 64) {
 #pragma unroll
-        for (int i = 0; i < kKStages; ++i) {
-            if (!ok || !mbar_wait(&sm->k_full[i], (tile + piece) & 1, a.p.status, &sm->abort)) {
-                ok = false;
-                continue;
+            for (int i = 0; i < kKStages; ++i) {
+                if (!ok || !mbar_wait(&sm->k_full[i], fills & 1, a.p.status, &sm->abort)) {
+                    ok = false;
+                    continue;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < kKBlocks; ++j) {
+                    const int kb = i * kKBlocks + j;
+                    if (kb >= kQTmem) continue;
+                    const uint64_t kd = sdesc_sw128(k_addr + i * kKStage + j * 2 * kBlk, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_copy(kQCol + 32 * kb + 8 * k, kd + 2 * k);
+                }
+                umma_commit(&sm->k_free[i]);
             }
+            ++fills;
+            if (!ok) break;
+        }
+        if (!mbar_wait(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
+        if (w.rows() <= 64) {
+            // (rows 64..127 take what follows in shared memory: rows of no token)
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < kKBlocks; ++j) {
-                const int kb = i * kKBlocks + j;
-                if (kb >= kQTmem) continue;
-                const uint64_t kd = sdesc_sw128(k_addr + i * kKStage + j * 2 * kBlk, 16, 1024);
+            for (int kb = 0; kb < kQTmem; ++kb)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_copy(kQCol + 32 * kb + 8 * k, kd + 2 * k);
-            }
-            umma_commit(&sm->k_free[i]);
+                for (int k = 0; k < 4; ++k)
+                    tmem_copy(kQCol + 32 * kb + 8 * k, sdesc_sw128(p_addr + kb * kBlk, 16, 1024) + 2 * k);
         }
-        if (!ok || !mbar_wait(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
-        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
+        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile, ++fills) {
             const uint32_t buf = tile % kSBufs;
             if (tile >= kSBufs && !mbar_wait(&sm->s_free[buf], (tile / kSBufs - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const uint32_t par = (tile + piece + 1) & 1;
-            ok = buf ? score_tile<1>(a, sm, q_addr, k_addr, par) : score_tile<0>(a, sm, q_addr, k_addr, par);
+            ok = buf ? score_tile<1>(a, sm, q_addr, k_addr, fills & 1) : score_tile<0>(a, sm, q_addr, k_addr, fills & 1);
         }
         if (ok) umma_commit(&sm->q_free);
     }
@@ -752,7 +811,7 @@ __device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const 
     for (Walk w(a, sm); ok && w.valid(); w.next()) {
         // lane i looks up box i of the tile's 128 rows, a tile ahead
         Box x = {a.p.n_pages, 0, false};
-        if (lane < 2 * boxes) x = find_box(a, w, w.k0 * kKeys + lane * a.box);
+        if (lane < 2 * boxes) x = it == 0 ? sm->plan_box[lane] : find_box(a, w.s, w.b, w.k0 * kKeys + lane * a.box);
         for (int kt = w.k0; ok && kt < w.k1; ++kt) {
             const int khs = w.keys(kt) > 64 ? 2 : 1;
             for (int g = 0; g < 2 * khs; ++g, ++it) {
@@ -767,7 +826,7 @@ __device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const 
                 if (i >= 0 && i < boxes)
                     tma_load_rows(v_sm + st * kVStage + i * a.box * 4 * 128, mv, &sm->v_full[st], 4 * d, x);
             }
-            if (kt + 1 < w.k1 && lane < 2 * boxes) x = find_box(a, w, (kt + 1) * kKeys + lane * a.box);
+            if (kt + 1 < w.k1 && lane < 2 * boxes) x = find_box(a, w.s, w.b, (kt + 1) * kKeys + lane * a.box);
         }
     }
     __syncwarp();
@@ -862,6 +921,26 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
     __syncwarp();
 }
 
+// 32 staged rows of 256 bytes (16-byte piece p of row i at p ^ (i & 15)) to memory,
+// two rows per instruction.
+__device__ __forceinline__ void put_rows(uint8_t *dst, int pitch, const uint8_t *st, int lane, int n_live) {
+    const int c = lane & 15;
+#pragma unroll
+    for (int b = 0; b < 32; b += 16) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = b + 2 * k + (lane >> 4);
+            v[k] = *reinterpret_cast<const uint4 *>(st + i * 256 + ((c ^ (i & 15)) << 4));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = b + 2 * k + (lane >> 4);
+            if (i < n_live) *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(i) * pitch + c * 16) = v[k];
+        }
+    }
+}
+
 // Warp w: rows 32 (w & 3) + lane, output dims 256 (w >> 2) .. + 255.
 __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, int cluster) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
@@ -923,11 +1002,10 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, int clu
                                                pack_bf16(u2f(x[i + 4]) * inv, u2f(x[i + 5]) * inv),
                                                pack_bf16(u2f(x[i + 6]) * inv, u2f(x[i + 7]) * inv));
                         }
+                        if (c == 128) fence_proxy_async_smem();  // (the slots are next written by a copy)
                         __syncwarp();
                         uint8_t *o = static_cast<uint8_t *>(a.p.out) + (row_w * kLatent + 256 * half + c) * 2;
-                        for (int i = lane >> 4; i < n_live; i += 2)
-                            *reinterpret_cast<uint4 *>(o + static_cast<int64_t>(i) * kLatent * 2 + (lane & 15) * 16) =
-                                *reinterpret_cast<const uint4 *>(st + i * 256 + (((lane & 15) ^ (i & 15)) << 4));
+                        put_rows(o, kLatent * 2, st, lane, n_live);
                         __syncwarp();
                     }
                 } else {
@@ -943,15 +1021,13 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, int clu
                                 *reinterpret_cast<uint4 *>(st + lane * 256 + (((8 * g + i / 4) ^ (lane & 15)) << 4)) =
                                     make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                         }
+                        if (c == 192) fence_proxy_async_smem();
                         __syncwarp();
-                        float *po = a.part_o + (pslot * kRows + 32 * quad) * kLatent + 256 * half + c;
-                        for (int i = lane >> 4; i < n_live; i += 2)
-                            *reinterpret_cast<uint4 *>(po + i * kLatent + (lane & 15) * 4) =
-                                *reinterpret_cast<const uint4 *>(st + i * 256 + (((lane & 15) ^ (i & 15)) << 4));
+                        put_rows(reinterpret_cast<uint8_t *>(a.part_o + (pslot * kRows + 32 * quad) * kLatent + 256 * half + c),
+                                 kLatent * 4, st, lane, n_live);
                         __syncwarp();
                     }
                 }
-                fence_proxy_async_smem();  // (the slots are next written by a copy)
             }
             if (live && half == 0) {
                 if (!whole) {
@@ -1049,9 +1125,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (warp < 8)
             score_softmax(a, sm, smem + kQBytes, map_rank(smem_u32(smem), 1));
         else if (warp == 8)
-            score_producer(a, sm, smem, smem + kQBytes + 2 * kPSlot, &mq, &mk);
+            score_producer(a, sm, smem, smem + kQBytes, smem + kQBytes + 2 * kPSlot, &mq, &mk);
         else if (warp == 9 && lane == 0)
-            score_mma(a, sm, smem, smem + kQBytes + 2 * kPSlot);
+            score_mma(a, sm, smem, smem + kQBytes, smem + kQBytes + 2 * kPSlot);
     } else {
         if (warp < 8)
             value_output(a, sm, smem, cluster);
@@ -1073,39 +1149,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Merge of the row tiles that a cut divided: o = sum_i 2^(m_i - M) o_i / sum_i
 // 2^(m_i - M) l_i over the parts, the first in its cluster's second slot, the
 // others in the next clusters' first slots.  One CTA per (cluster, 4 rows); most
-// find nothing to do.
-constexpr int kMergeRows = 4;
+// find nothing to do.  Bound by latency: two round trips to L2.
+constexpr int kMergeRows = 4;   // 128 threads each
+constexpr int kMaxParts = 256;  // clusters of any GPU this runs on
 
-__global__ void __launch_bounds__(256) paged_mla_merge_kernel(const TcArgs a) {
+__global__ void __launch_bounds__(128 * kMergeRows) paged_mla_merge_kernel(const TcArgs a) {
+    __shared__ float wt[kMergeRows][kMaxParts];
     griddep_wait();
     const int c = blockIdx.x;
     const Meta me = a.meta[c];
-    if (me.parts == 0) return;
-    const int d = (threadIdx.x & 127) * 4;
-#pragma unroll 1
-    for (int k = 0; k < kMergeRows / 2; ++k) {
-        const int r = blockIdx.y * kMergeRows + 2 * k + (threadIdx.x >> 7);
-        if (r >= me.rows) continue;
-        auto slot = [&](int i) { return static_cast<int64_t>(2 * (c + i) + (i == 0 ? 1 : 0)) * kRows + r; };
-        float M = -INFINITY;
-        for (int i = 0; i < me.parts; ++i) M = fmaxf(M, a.part_ml[slot(i) * 2]);
-        float L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (M != -INFINITY)
-            for (int i = 0; i < me.parts; ++i) {
-                const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(i) * 2);
-                if (ml.x == -INFINITY) continue;
-                const float wt = exp2f(ml.x - M);
-                const float4 x = *reinterpret_cast<const float4 *>(a.part_o + slot(i) * kLatent + d);
-                L += wt * ml.y;
-                acc.x += wt * x.x, acc.y += wt * x.y, acc.z += wt * x.z, acc.w += wt * x.w;
-            }
+    const int g = threadIdx.x >> 7, r = blockIdx.y * kMergeRows + g;
+    if (blockIdx.y * kMergeRows >= me.rows || me.parts == 0) return;
+    const int d = (threadIdx.x & 127) * 4, lane = threadIdx.x & 31;
+    const int64_t slot0 = static_cast<int64_t>(2 * c + 1) * kRows + r;                        // the first part
+    auto slot = [&](int i) { return i == 0 ? slot0 : static_cast<int64_t>(2 * (c + i)) * kRows + r; };
+    // the first eight parts' values are on their way while the weights are found
+    float4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = i < me.parts ? *reinterpret_cast<const float4 *>(a.part_o + slot(i) * kLatent + d)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((threadIdx.x & 127) < 32) {
+        float M = -INFINITY, L = 0.f;
+        for (int i = lane; i < me.parts; i += 32) M = fmaxf(M, a.part_ml[slot(i) * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int i = lane; i < me.parts; i += 32) {
+            const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(i) * 2);
+            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+            wt[g][i] = w;
+            L += w * ml.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         const float inv = L > 0.f ? 1.f / L : 0.f;
-        const int64_t row = static_cast<int64_t>(me.row0) + r;
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.p.out) + row * kLatent + d) =
-            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        if (d == 0 && a.p.lse) a.p.lse[row] = L > 0.f ? M * kLn2 + logf(L) : -INFINITY;
+        for (int i = lane; i < me.parts; i += 32) wt[g][i] *= inv;
+        if (lane == 0 && r < me.rows && a.p.lse)
+            a.p.lse[static_cast<int64_t>(me.row0) + r] = L > 0.f ? M * kLn2 + logf(L) : -INFINITY;
     }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4 &v, float w) {
+        // (a part without weight may have left anything, and 0 x NaN is NaN)
+        if (w != 0.f) acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < me.parts) add(x[i], wt[g][i]);
+    for (int i0 = 8; i0 < me.parts; i0 += 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i < me.parts) x[i] = *reinterpret_cast<const float4 *>(a.part_o + slot(i0 + i) * kLatent + d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i < me.parts) add(x[i], wt[g][i0 + i]);
+    }
+    if (r < me.rows)
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.p.out) + (static_cast<int64_t>(me.row0) + r) * kLatent + d) =
+            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1122,7 +1223,7 @@ bool paged_mla_tc_shape(const PagedMlaArgs &a) {
 }
 
 size_t paged_mla_tc_scratch(int num_sms) {
-    const size_t c = num_sms / 2;
+    const size_t c = std::min(num_sms / 2, kMaxParts);
     return align256(c * sizeof(Meta)) + align256(2 * c * kRows * 2 * sizeof(float)) + 2 * c * kRows * kLatent * sizeof(float);
 }
 
@@ -1131,7 +1232,7 @@ cudaError_t launch_paged_mla_tc(const PagedMlaArgs &p, void *scratch, int num_sm
     if (!enc) return cudaErrorNotSupported;
     TcArgs a;
     a.p = p;
-    a.clusters = num_sms / 2;
+    a.clusters = std::min(num_sms / 2, kMaxParts);
     a.tok_tile = kRows / p.heads;
     a.box = 64;
     while (p.page_rows % a.box != 0) a.box >>= 1;
@@ -1166,7 +1267,7 @@ cudaError_t launch_paged_mla_tc(const PagedMlaArgs &p, void *scratch, int num_sm
     if (e != cudaSuccess) return e;
     e = launch_pdl(paged_mla_tc_kernel, dim3(2 * a.clusters), dim3(kThreads), kBig + sizeof(Small), st, a, mq, mk, mv);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_mla_merge_kernel, dim3(a.clusters, kRows / kMergeRows), dim3(256), 0, st, a);
+    return launch_pdl(paged_mla_merge_kernel, dim3(a.clusters, kRows / kMergeRows), dim3(128 * kMergeRows), 0, st, a);
 }
 
 }  // namespace dsa
