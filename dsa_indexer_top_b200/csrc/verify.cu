@@ -8,6 +8,7 @@
 #include <cfloat>
 #include <climits>
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -18,22 +19,35 @@
 namespace dsa {
 namespace {
 
+// A cluster of CTAs per request.  One pass over the one row pair that decides the
+// token: each warp sums a contiguous segment of the vocabulary; the segments' sums go
+// to every CTA of the cluster, the one whose segment crosses the target reads that
+// segment (1/16 of its share, still in L2) once more and finds the token by a scan of
+// per-thread runs.  Bound by memory: 4 or 2 bytes per entry and row, and by latency
+// (three dependent round trips) for few requests.
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
+constexpr int kVerMaxCluster = 8;
+constexpr int kVerUnroll = 8;  // loads of a row in flight per thread
 
 // A probability as float64; negative, NaN and infinite values count as 0.
 __device__ __forceinline__ double prob(float x) { return x > 0.f && x <= FLT_MAX ? static_cast<double>(x) : 0.0; }
-__device__ __forceinline__ float ld_p(const float *p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float ld_p(const __nv_bfloat16 *p, int64_t i) { return __bfloat162float(p[i]); }
+__device__ __forceinline__ float ld_p(const float *p, int64_t i) { return __ldg(p + i); }
+__device__ __forceinline__ float ld_p(const __nv_bfloat16 *p, int64_t i) {
+    return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short *>(p) + i)) << 16);
+}
 
-// One CTA per request; each warp holds a contiguous segment of the vocabulary.
 template <typename T>
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a) {
-    __shared__ double seg[kVerWarps];
-    __shared__ int last_s[kVerWarps];
-    __shared__ int acc_s;
+    namespace cg = cooperative_groups;
+    __shared__ double seg[kVerMaxCluster * kVerWarps];
+    __shared__ int last_s[kVerMaxCluster * kVerWarps];
+    __shared__ double run[kVerWarps];
+    __shared__ int acc_s, chosen_s;
+    cg::cluster_group cluster = cg::this_cluster();
     const dsa_verify &v = a.v;
-    const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int CL = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int r = blockIdx.x / CL, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_wait();
     const int D = v.n_draft, V = v.vocab;
     const T *pt = static_cast<const T *>(v.target) + r * v.t_req_stride;
@@ -62,6 +76,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
         acc = min(acc, n);
         if (lane == 0) acc_s = acc;
     }
+    if (tid == 0) chosen_s = -1;
     __syncthreads();
     const int acc = acc_s;
     const bool rejected = acc < n;
@@ -75,78 +90,144 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
         else if (!qt)
             gone = t;
     }
-    const int per = ((V + kVerWarps - 1) / kVerWarps + 31) / 32 * 32;
-    const int j0 = min(warp * per, V), j1 = min(j0 + per, V);
-    int chosen = -1;
-    for (int pass = 0; pass < 2 && chosen < 0; ++pass) {
-        // pass 1 only where the residual has no weight: the target's own row
+    const float u = v.sample_u[r];
+    const int nw = CL * kVerWarps;
+    const int per = ((V + nw - 1) / nw + 31) / 32 * 32;  // a warp's segment
+    const int gw = rank * kVerWarps + warp;
+    const int j0 = static_cast<int>(min(static_cast<int64_t>(gw) * per, static_cast<int64_t>(V)));
+    const int j1 = min(j0 + per, V);
+    bool writer = false;
+    for (int pass = 0; pass < 2; ++pass) {
+        // the second pass only where the residual has no weight: the target's own row
         const T *qr = pass == 0 ? qrow : nullptr;
         const int skip = pass == 0 ? gone : -1;
-        auto weight = [&](int j) -> double {
-            if (j == skip) return 0.0;
-            const double p = prob(ld_p(prow, j));
-            return qr ? fmax(p - prob(ld_p(qr, j)), 0.0) : p;
+        auto weight = [&](float p, float q, int j) -> double {
+            const double w = prob(p) - (qr ? prob(q) : 0.0);
+            return w > 0.0 && j != skip ? w : 0.0;
         };
         double s = 0.0;
         int last = -1;
-        for (int j = j0 + lane; j < j1; j += 32) {
-            const double w = weight(j);
-            s += w;
-            if (w > 0.0) last = j;
+        for (int b = j0 + lane; b < j1; b += 32 * kVerUnroll) {
+            float p[kVerUnroll], q[kVerUnroll];
+#pragma unroll
+            for (int k = 0; k < kVerUnroll; ++k) {
+                const int j = b + 32 * k;
+                p[k] = j < j1 ? ld_p(prow, j) : 0.f;
+                q[k] = qr && j < j1 ? ld_p(qr, j) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kVerUnroll; ++k) {
+                const double w = weight(p[k], q[k], b + 32 * k);
+                s += w;
+                if (w > 0.0) last = b + 32 * k;
+            }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             s += __shfl_xor_sync(0xffffffffu, s, o);
             last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
         }
-        __syncthreads();
-        if (lane == 0) seg[warp] = s, last_s[warp] = last;
-        __syncthreads();
+        if (pass > 0) cluster.sync();  // every CTA has read the first pass's sums
+        if (lane < CL) {
+            *cluster.map_shared_rank(&seg[gw], lane) = s;
+            *cluster.map_shared_rank(&last_s[gw], lane) = last;
+        }
+        cluster.sync();
+        // every warp alike: total weight, then the segment that crosses the target
         double total = 0.0;
         int any = -1;
-        for (int w = 0; w < kVerWarps; ++w) {
+        for (int w = 0; w < nw; ++w) {
             total += seg[w];
             any = max(any, last_s[w]);
         }
-        if (any < 0) continue;  // no weight at all
-        const float u = v.sample_u[r];
+        if (any < 0 && pass == 0) continue;  // no weight at all (the same in every CTA)
+        if (any < 0) {
+            writer = rank == 0;
+            break;
+        }
         const double target = (u > 0.f ? static_cast<double>(u) : 0.0) * total;
-        // the segment that crosses the target, scanned by every warp alike
         double before = 0.0;
         int sg = 0;
-        for (; sg < kVerWarps - 1 && !(before + seg[sg] > target); ++sg) before += seg[sg];
-        const int k0 = min(sg * per, V), k1 = min(k0 + per, V);
-        for (int b = k0; b < k1 && chosen < 0; b += 32) {
-            double c = b + lane < k1 ? weight(b + lane) : 0.0;
-            const bool some = c > 0.0;
+        for (; sg < nw - 1 && !(before + seg[sg] > target); ++sg) before += seg[sg];
+        writer = sg / kVerWarps == rank;
+        if (!writer) break;
+        // a run of entries per thread, a scan of the runs' sums
+        const int k0 = static_cast<int>(min(static_cast<int64_t>(sg) * per, static_cast<int64_t>(V)));
+        const int k1 = min(k0 + per, V);
+        const int len = (per + kVerThreads - 1) / kVerThreads;
+        const int a0 = min(k0 + tid * len, k1), a1 = min(a0 + len, k1);
+        double c = 0.0;
+        for (int j = a0; j < a1; ++j) c += weight(ld_p(prow, j), qr ? ld_p(qr, j) : 0.f, j);
+        double inc = c;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, c, o);
-                if (lane >= o) c += y;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, some && before + c > target);
-            if (hit) chosen = b + __ffs(hit) - 1;
-            before += __shfl_sync(0xffffffffu, c, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
         }
-        // (a sum rounded past the total, or u >= 1: the last token with weight)
-        if (chosen < 0 || chosen > any) chosen = any;
+        if (lane == 31) run[warp] = inc;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) before += run[w];
+        const double start = before + (inc - c);
+        if (c > 0.0 && before + inc > target && !(start > target)) {
+            // this run crosses: its first entry past the target (its last with weight
+            // where rounding leaves none)
+            double t = start;
+            int pick = -1;
+            for (int j = a0; j < a1; ++j) {
+                const double w = weight(ld_p(prow, j), qr ? ld_p(qr, j) : 0.f, j);
+                t += w;
+                if (w > 0.0) {
+                    pick = j;
+                    if (t > target) break;
+                }
+            }
+            atomicMax(&chosen_s, pick);
+        }
+        __syncthreads();
+        // (no run crosses where the sums round past the total, or u >= 1: the last entry
+        // with weight)
+        if (tid == 0 && chosen_s < 0) chosen_s = any;
+        __syncthreads();
+        break;
     }
+    cluster.sync();  // no CTA leaves while another may write to it
+    if (!writer) return;
+    const int chosen = chosen_s;
     if (chosen < 0) bad = true;
-    for (int i = threadIdx.x; i <= D; i += kVerThreads)
+    for (int i = tid; i <= D; i += kVerThreads)
         v.tokens[static_cast<int64_t>(r) * (D + 1) + i] = i < acc ? x[i] : i == acc ? chosen : -1;
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         v.n_accept[r] = acc;
         if (bad) report_status(a.status, DSA_ERR_INVALID);
     }
 }
 
+template <typename T>
+cudaError_t launch_verify_t(const VerifyArgs &a, int num_sms, cudaStream_t st) {
+    // as many CTAs per request as keep them all resident (four of 512 threads per SM)
+    int cl = kVerMaxCluster;
+    while (cl > 1 && static_cast<int64_t>(a.v.n_req) * cl > 4 * static_cast<int64_t>(num_sms)) cl >>= 1;
+    if (static_cast<int64_t>(a.v.n_req) * cl > INT_MAX) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.v.n_req) * cl);
+    cfg.blockDim = dim3(kVerThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cl;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a);
+}
+
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs &a, int num_sms, cudaStream_t st) {
-    (void)num_sms;
-    if (a.v.dtype == DSA_BF16)
-        return launch_pdl(verify_kernel<__nv_bfloat16>, dim3(a.v.n_req), dim3(kVerThreads), 0, st, a);
-    return launch_pdl(verify_kernel<float>, dim3(a.v.n_req), dim3(kVerThreads), 0, st, a);
+    return a.v.dtype == DSA_BF16 ? launch_verify_t<__nv_bfloat16>(a, num_sms, st) : launch_verify_t<float>(a, num_sms, st);
 }
 
 }  // namespace dsa
