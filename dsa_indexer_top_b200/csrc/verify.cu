@@ -5,6 +5,7 @@
 // lowest j with sum_{k<=j} w_k > u sum_k w_k, w = max(p_i - q_i, 0); with every
 // draft accepted w = p_n.  The weights are summed in float64, so that neither the
 // order of summation nor a float32 rounding decides the token.
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 
@@ -22,11 +23,12 @@ namespace {
 // A cluster of CTAs per request.  One pass over the one row pair that decides the
 // token: each warp sums a contiguous segment of the vocabulary; the segments' sums go
 // to every CTA of the cluster, the one whose segment crosses the target reads that
-// segment (1/16 of its share, still in L2) once more and finds the token by a scan of
+// segment (an eighth of its share, still in L2) once more and finds the token by a scan of
 // per-thread runs.  Bound by memory: 4 or 2 bytes per entry and row, and by latency
 // (three dependent round trips) for few requests.
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
+constexpr int kVerPerSm = 4;  // CTAs per SM (64 registers a thread)
 constexpr int kVerMaxCluster = 8;
 constexpr int kVerUnroll = 8;  // loads of a row in flight per thread
 
@@ -204,9 +206,9 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
 
 template <typename T>
 cudaError_t launch_verify_t(const VerifyArgs &a, int num_sms, cudaStream_t st) {
-    // as many CTAs per request as keep them all resident (four of 512 threads per SM)
-    int cl = kVerMaxCluster;
-    while (cl > 1 && static_cast<int64_t>(a.v.n_req) * cl > 4 * static_cast<int64_t>(num_sms)) cl >>= 1;
+    // as many CTAs per request as are all resident at once
+    const int64_t slots = static_cast<int64_t>(kVerPerSm) * num_sms;
+    const int cl = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kVerMaxCluster, slots / a.v.n_req)));
     if (static_cast<int64_t>(a.v.n_req) * cl > INT_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.v.n_req) * cl);
