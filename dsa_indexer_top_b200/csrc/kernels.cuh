@@ -296,7 +296,7 @@ struct PagedMlaArgs {
 cudaError_t launch_paged_mla_generic(const PagedMlaArgs &a, cudaStream_t st);
 // Tensor-core path: the shapes it takes, its scratch, and the launch.
 bool paged_mla_tc_shape(const PagedMlaArgs &a);
-size_t paged_mla_tc_scratch(int num_sms);
+size_t paged_mla_tc_scratch(const PagedMlaArgs &a, int num_sms);
 cudaError_t launch_paged_mla_tc(const PagedMlaArgs &a, void *scratch, int num_sms, cudaStream_t st);
 
 // ------------------------------------------------------------------ draft verification

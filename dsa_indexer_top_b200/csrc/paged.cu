@@ -410,7 +410,8 @@ dsa_status dsa_page_tables(const dsa_page_plan *p, void *ws, size_t ws_bytes, vo
 
 size_t dsa_paged_mla_workspace_bytes(const dsa_paged_batch *batch, const dsa_mla *mla) {
     if (check_batch(batch) != DSA_OK || check_mla_layers(mla, 1) != DSA_OK) return 0;
-    return kStatus + (paged_mla_tc_shape(paged_args(batch, mla, nullptr)) ? paged_mla_tc_scratch(sm_count_current()) : 0);
+    const PagedMlaArgs a = paged_args(batch, mla, nullptr);
+    return kStatus + (paged_mla_tc_shape(a) ? paged_mla_tc_scratch(a, sm_count_current()) : 0);
 }
 
 dsa_status dsa_paged_mla(const dsa_paged_batch *batch, const dsa_mla *mla, void *ws, size_t ws_bytes, void *stream) {

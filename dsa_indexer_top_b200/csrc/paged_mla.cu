@@ -36,8 +36,11 @@
 #include <algorithm>
 #include <cfloat>
 #include <climits>
+#include <cstddef>
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -60,6 +63,13 @@ constexpr int kVStages = 5;
 constexpr int kPSlot = 4 * kBlk;                 // 128 rows x 128 keys
 constexpr int kBig = kQBytes + 2 * kPSlot + kKStages * kKStage;
 static_assert(kBig == 2 * kPSlot + kVStages * kVStage, "both CTAs fill the same space");
+// Packed FP8 rows, score CTA: two tiles of codes (128 keys x 512 bytes), one of RoPE
+// keys; value CTA: units of 32 keys, codes as they come and widened to fp16.
+constexpr int kCodes = 8 * kBlk;
+constexpr int kRawStage = 2 * kBlk, kRawStages = 4;
+constexpr int kHStage = 4 * kBlk, kHStages = 3;
+static_assert(kBig == kQBytes + 2 * kPSlot + 2 * kCodes + 2 * kBlk, "shared memory, FP8 score CTA");
+static_assert(kBig == 2 * kPSlot + kRawStages * kRawStage + kHStages * kHStage, "shared memory, FP8 value CTA");
 constexpr int kSmemMax = 232448;                 // 227 KB
 constexpr int kThreads = 384;                    // 8 softmax / output warps; producer, MMA, 2 idle
 constexpr int kSBufs = 2;
@@ -69,10 +79,17 @@ static_assert(kQCol + 32 * kQTmem <= 512, "tensor memory");
 // costs the pair a stop): weights below 2^32 over 2^20 rows stay far inside float32
 // and bf16, whose precision does not depend on the scale.
 constexpr float kRescale = 32.0f;
+// Packed FP8 rows: a weight times its row's scale goes to the MMA as fp16, 2^4 at the
+// reference maximum: below 2^15 (with a scale's mantissa) until that is raised, and
+// rounded to fp16's smallest step only 2^-28 under it.
+constexpr float kRescaleFp8 = 10.0f;
+constexpr float kShiftFp8 = 4.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kIdescS = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(128, 256, false, true);
+constexpr uint32_t kIdescS8 = idesc_e4m3(128, 128);
+constexpr uint32_t kIdescO16 = idesc_f16(128, 256, false, true);
 
 enum { kCmdRescale = 0, kCmdFinish = 1, kCmdExit = 2 };
 
@@ -98,6 +115,9 @@ struct Small {
     // value CTA
     uint64_t p_full[2], v_full[kVStages], v_free[kVStages], cmd_full, cmd_done, stat_full;
     uint64_t fin;
+    // packed FP8 rows
+    uint64_t sig_full[2], sig_free[2];                // score CTA: row scales of the tiles of either parity
+    uint64_t h_full[kHStages], h_free[kHStages];      // value CTA: widened units
     uint32_t tmem_base;
     int abort;
     int plan_b, plan_rt, plan_k0, plan_active;
@@ -108,8 +128,8 @@ struct Small {
     int flags[2][4];          // value CTA: [slot][quadrant] some row's O must be rescaled
     uint32_t key_ok[kSBufs];  // score CTA: [S buffer] bit i: keys 8i..8i+7 are in the pool
     union {
-        struct {
-            float m_run[kRows], m_odd[kRows], l_odd[kRows];  // score CTA
+        struct alignas(16) {  // (the scales are read 16 bytes at a time)
+            float m_run[kRows], l_odd[kRows], sigma[2][kKeys];  // score CTA
         } q;
         struct {
             float alpha[2][kRows];  // value CTA: [slot][row]
@@ -118,6 +138,7 @@ struct Small {
     };
 };
 static_assert(kBig + sizeof(Small) <= kSmemMax, "shared memory");
+static_assert(offsetof(Small, q.sigma) % 16 == 0, "row scales");
 
 struct Meta {  // a row tile whose first part ends its cluster's range
     int parts, row0, rows, pad;
@@ -131,6 +152,8 @@ struct TcArgs {
     Meta *meta;         // [clusters]
     float *part_ml;     // [2 * clusters][128][2] maximum (log2), sum
     float *part_o;      // [2 * clusters][128][512]
+    const uint8_t *q8;  // packed FP8 rows: the queries' latent part as two E4M3 terms [rows][2][512]
+    const float *q8_scale;  // [rows] their power-of-two scale
 };
 
 // ------------------------------------------------------------------ cluster PTX
@@ -167,6 +190,16 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with 8-bit E4M3 operands (four values per column).
+__device__ __forceinline__ void umma_e4m3_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -217,6 +250,15 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// Two E4M3 codes as two fp16 (exact).
+__device__ __forceinline__ uint32_t widen2(uint32_t two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -454,6 +496,15 @@ __device__ __forceinline__ void tma_load_rows(void *dst, const CUtensorMap *map,
         : "memory");
 }
 
+// The RoPE keys of packed FP8 rows: [8-row group][8 rows][128 bytes].
+__device__ __forceinline__ void tma_load_rope(void *dst, const CUtensorMap *map, uint64_t *bar, const Box &x) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(0), "r"(x.group), "r"(x.page)
+        : "memory");
+}
+
 // ------------------------------------------------------------------ score CTA
 // Stage i of the ring holds blocks 3i..3i+2 of the key tiles, and of the query tile
 // before them: constant addresses let the MMA thread issue at full rate.
@@ -643,11 +694,197 @@ __device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *p_
     mbar_wait(&sm->fin, 0, a.p.status, nullptr);
 }
 
+// Packed FP8 rows, score CTA.  q = s (q1 + q2) with q1, q2 in E4M3 and s a power of
+// two: a bf16 value's eight significant bits are two terms of four, so the latent
+// logits come from the codes as they are, two 8-bit MMAs (K = 32, 64 cycles) in the
+// place of two 16-bit ones, and nothing is widened here.  The RoPE part has its own
+// accumulator (the row scale applies to the latent part alone), which leaves room
+// for one S buffer.  Barriers 0 and 1 of the ring: codes of the tiles of either
+// parity; 2: RoPE keys.
+__device__ void score_producer_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *p_stage, uint8_t *c_sm, uint8_t *r_sm,
+                                   const CUtensorMap *mq, const CUtensorMap *mq8, const CUtensorMap *mk,
+                                   const CUtensorMap *mr) {
+    const int lane = threadIdx.x & 31;
+    const int boxes = kKeys / a.box;
+    uint32_t fills[3] = {0, 0, 0};
+    uint32_t tile = 0, piece = 0, q_use = 0;
+    bool ok = true;
+    auto stage_free = [&](int i) {
+        return fills[i] == 0 || mbar_wait(&sm->k_free[i], (fills[i] - 1) & 1, a.p.status, &sm->abort);
+    };
+    for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
+        Box x = {a.p.n_pages, 0, false};
+        if (lane < boxes) x = piece == 0 ? sm->plan_box[lane] : find_box(a, w.s, w.b, w.k0 * kKeys + lane * a.box);
+        const bool small = w.rows() <= 64;
+        const int qrow = static_cast<int>(w.row0());
+        // more than 64 rows: q1 through one code stage, q2 through the other; else both
+        // through the space where P is staged
+        if (!small) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!ok || !stage_free(i)) {
+                    ok = false;
+                    continue;
+                }
+                ++fills[i];
+                if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[i], kCodes);
+                __syncwarp();
+                if (lane < 8)
+                    tma_load_2d(c_sm + i * kCodes + lane * kBlk, mq8, &sm->k_full[i], 512 * i + 128 * (lane >> 1),
+                                qrow + 64 * (lane & 1));
+            }
+            if (!ok) break;
+        }
+        auto load_query = [&]() {
+            if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) return false;
+            if (small)  // the staged P of the last two tiles has left
+                for (uint32_t t = tile > 2 ? tile - 2 : 0; t < tile; ++t)
+                    if (!mbar_wait_cluster(&sm->p_got[t & 1], (t >> 1) & 1, a.p.status, &sm->abort)) return false;
+            ++q_use;
+            if (lane == 0) mbar_arrive_expect_tx(&sm->q_full, (small ? 9 : 2) * kBlk);
+            __syncwarp();
+            if (small && lane < 8) tma_load_2d(p_stage + lane * kBlk, mq8, &sm->q_full, 128 * lane, qrow);
+            if (lane >= 8 && lane < (small ? 9 : 10))
+                tma_load_2d(q_sm + (lane - 8) * kBlk, mq, &sm->q_full, kLatent, qrow + 64 * (lane - 8));
+            return true;
+        };
+        if (piece == 0 || !small) ok = load_query();
+        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
+            const int need = w.keys(kt) > 64 ? kKeys : 64;
+            if (__any_sync(0xffffffffu, x.missing) && lane == 0) report_status(a.p.status, DSA_ERR_INVALID);
+            const int st = tile & 1;
+            if (!(st ? stage_free(1) : stage_free(0))) {
+                ok = false;
+                break;
+            }
+            if (st)
+                ++fills[1];
+            else
+                ++fills[0];
+            if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[st], need * 512);
+            __syncwarp();
+            if (lane * a.box < need) tma_load_rows(c_sm + st * kCodes + lane * a.box * 512, mk, &sm->k_full[st], 0, x);
+            if (!stage_free(2)) {
+                ok = false;
+                break;
+            }
+            ++fills[2];
+            if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[2], need * 128);
+            __syncwarp();
+            if (lane * a.box < need) tma_load_rope(r_sm + lane * a.box * 128, mr, &sm->k_full[2], x);
+            if (kt == w.k0 && piece > 0 && small && !load_query()) {
+                ok = false;
+                break;
+            }
+            if (kt + 1 < w.k1 && lane < boxes) x = find_box(a, w.s, w.b, (kt + 1) * kKeys + lane * a.box);
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (fills[i] > 0) mbar_wait(&sm->k_full[i], (fills[i] - 1) & 1, a.p.status, nullptr);
+    if (q_use > 0) mbar_wait(&sm->q_full, (q_use - 1) & 1, a.p.status, nullptr);
+}
+
+// Row scales of every key tile to shared memory, 0 for a row nobody sees.
+__device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
+    const int lane = threadIdx.x & 31;
+    uint32_t tile = 0;
+    const uint8_t *kv = static_cast<const uint8_t *>(a.p.kv) + kFp8ScaleOff;
+    for (Walk w(a, sm); w.valid(); w.next())
+        for (int kt = w.k0; kt < w.k1; ++kt, ++tile) {
+            const int s0 = kt * kKeys + 4 * lane;
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            const Box x = find_box(a, w.s, w.b, s0);  // (four rows of one 8-row group)
+            if (x.page < a.p.n_pages) {
+                const uint8_t *row = kv + x.page * a.p.kv_page_stride + (8 * x.group + (s0 & 7)) * a.p.kv_row_stride;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (s0 + i < w.s.len) v[i] = __ldg(reinterpret_cast<const float *>(row + i * a.p.kv_row_stride));
+            }
+            if (tile >= 2 && !mbar_wait(&sm->sig_free[tile & 1], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) return;
+            *reinterpret_cast<float4 *>(&sm->q.sigma[tile & 1][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->sig_full[tile & 1]);
+        }
+}
+
+template <int kSt>
+__device__ __forceinline__ bool score_tile_fp8(const TcArgs &a, Small *sm, uint32_t q_addr, uint32_t c_addr, uint32_t r_addr,
+                                               uint32_t parity, uint32_t parity_rope) {
+    if (!mbar_wait(&sm->k_full[kSt], parity, a.p.status, &sm->abort)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < kLatent / 32; ++k) {
+        const uint64_t bd = sdesc_sw128(c_addr + kSt * kCodes + (k >> 2) * 1024, 16, 4096) + 2 * (k & 3);
+        umma_e4m3_ta(0, kQCol + 8 * k, bd, kIdescS8, k > 0 ? 1u : 0u);
+        umma_e4m3_ta(0, kQCol + 128 + 8 * k, bd, kIdescS8, 1u);
+    }
+    umma_commit(&sm->k_free[kSt]);
+    if (!mbar_wait(&sm->k_full[2], parity_rope, a.p.status, &sm->abort)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        umma_bf16(kKeys, sdesc_sw128(q_addr, 16, 1024) + 2 * k, sdesc_sw128(r_addr, 16, 1024) + 2 * k, kIdescS, k > 0 ? 1u : 0u);
+    umma_commit(&sm->k_free[2]);
+    umma_commit(&sm->s_full[kSt]);
+    return true;
+}
+
+__device__ void score_mma_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *p_stage, uint8_t *c_sm, uint8_t *r_sm) {
+    const uint32_t q_addr = smem_u32(q_sm), c_addr = smem_u32(c_sm), r_addr = smem_u32(r_sm), p_addr = smem_u32(p_stage);
+    uint32_t tile = 0, piece = 0, fill0 = 0, fill1 = 0;
+    bool ok = true;
+    for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
+        if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
+        if (w.rows() > 64) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!ok || !mbar_wait(&sm->k_full[i], (i ? fill1 : fill0) & 1, a.p.status, &sm->abort)) {
+                    ok = false;
+                    continue;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    tmem_copy(kQCol + 128 * i + 8 * k,
+                              sdesc_sw128(c_addr + i * kCodes + (k >> 2) * 2 * kBlk, 16, 1024) + 2 * (k & 3));
+                umma_commit(&sm->k_free[i]);
+            }
+            ++fill0;
+            ++fill1;
+            if (!ok) break;
+        }
+        if (!mbar_wait(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
+        if (w.rows() <= 64) {
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                tmem_copy(kQCol + 8 * k, sdesc_sw128(p_addr + (k >> 2) * kBlk, 16, 1024) + 2 * (k & 3));
+        }
+        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
+            if (tile >= 1 && !mbar_wait(&sm->s_free[0], (tile - 1) & 1, a.p.status, &sm->abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (tile & 1)
+                ok = score_tile_fp8<1>(a, sm, q_addr, c_addr, r_addr, fill1++ & 1, tile & 1);
+            else
+                ok = score_tile_fp8<0>(a, sm, q_addr, c_addr, r_addr, fill0++ & 1, tile & 1);
+        }
+        if (ok) umma_commit(&sm->q_free);
+    }
+    umma_commit(&sm->fin);
+    mbar_wait(&sm->fin, 0, a.p.status, nullptr);
+}
+
 // Softmax.  Warps 0-3 take the even tiles, 4-7 the odd ones, so that one tile's
 // exponentials run beside the next one's loads and exchanges; thread r of a group
 // holds row r's 128 logits.  The running maxima pass from tile to tile through
 // shared memory; each group keeps the sum of its own tiles, relative to the maximum
 // it saw last.
+template <bool kFp8>
 __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint32_t p_remote) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, group = warp >> 2;
     const int r = 32 * quad + lane;
@@ -665,27 +902,54 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         const int tok = w.rt * a.tok_tile + min(r, rows - 1) / a.p.heads;
         const int pos = w.s.len - w.s.n + tok;
         const int pos0 = w.s.len - w.s.n + w.rt * a.tok_tile;  // the tile's first token
+        const float qc2 = kFp8 ? c2 * a.q8_scale[w.row0() + min(r, rows - 1)] : 0.f;
         float m = -INFINITY, l = 0.f;
         for (int kt = w.k0; kt < w.k1; ++kt, ++tile) {
             const uint32_t slot = tile & 1;  // of P, and of the S buffers
+            const uint32_t sbuf = kFp8 ? 0 : slot;  // (its barrier of arrivals; s_full is by tile parity)
             if (slot != static_cast<uint32_t>(group)) continue;
-            if (!mbar_wait(&sm->s_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
+            if ((kFp8 && !mbar_wait(&sm->sig_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) ||
+                !mbar_wait(&sm->s_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const uint32_t okbits = *reinterpret_cast<volatile uint32_t *>(&sm->key_ok[slot]);
+            const uint32_t okbits = kFp8 ? 0xFFFFu : *reinterpret_cast<volatile uint32_t *>(&sm->key_ok[slot]);
+            const float *sig = sm->q.sigma[slot];
             const int nk = w.keys(kt);
             uint32_t x[128];
-            if (live) {
+            if (live && !kFp8) {
 #pragma unroll
                 for (int c = 0; c < 128; c += 32)
                     tmem_ld32(tb + kKeys * slot + c, reinterpret_cast<uint32_t(&)[32]>(x[c]));
                 tmem_ld_wait();
             }
+            if (live && kFp8) {
+                // log2 of weight times 2^e, the row scale's power of two, which bounds what the
+                // MMA gets: c2 (s sigma S_lat + S_rope) + e
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t y[32];
+                    tmem_ld32(tb + c, reinterpret_cast<uint32_t(&)[32]>(x[c]));
+                    tmem_ld32(tb + kKeys + c, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 g4 = *reinterpret_cast<const float4 *>(sig + c + i);
+                        const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            // exponent as a float: its biased value in the low bits of 2^23
+                            const float e = u2f(0x4B000000u | (__float_as_uint(g[k]) >> 23)) - (8388608.f + 127.f);
+                            const float t = fmaf(u2f(x[c + i + k]) * g[k], qc2, fmaf(u2f(y[i + k]), c2, e));
+                            x[c + i + k] = g[k] > 0.f ? __float_as_uint(t) : 0xFF800000u;
+                        }
+                    }
+                }
+            }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->s_free[slot]);
+            if (lane == 0) mbar_arrive(&sm->s_free[sbuf]);
             float mx = -INFINITY;
             if (live) {
                 const int s0 = kt * kKeys;
@@ -699,7 +963,8 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                 for (int i = 0; i < 128; i += 4)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], u2f(x[i + k]));
-                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;  // (scale > 0)
+                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                if (!kFp8) mx *= c2;  // (scale > 0)
             }
             // the previous tile's running maximum
             float mp = -INFINITY;
@@ -713,7 +978,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             float mn = mp, al = 1.f;
             if (mp == -INFINITY) {
                 mn = mx;  // nothing accumulated for the row yet
-            } else if (r < rows && mx > mp + kRescale) {
+            } else if (r < rows && mx > mp + (kFp8 ? kRescaleFp8 : kRescale)) {
                 al = ex2(mp - mx);
                 mn = mx;
             }
@@ -729,7 +994,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                 break;
             }
             if (live) {
-                const float mu = m == -INFINITY ? 0.f : m;
+                const float mu = (m == -INFINITY ? 0.f : m) - (kFp8 ? kShiftFp8 : 0.f);
                 float l4[4] = {l, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
@@ -740,19 +1005,34 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                         float p[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            p[i] = ex2(fmaf(u2f(x[64 * hf + 8 * c + i]), c2, -mu));
-                            l4[i & 3] += p[i];
+                            if (kFp8) {
+                                // weight = 2^x / 2^e; the codes' weight has the whole scale
+                                const float g = sig[64 * hf + 8 * c + i];
+                                const float re = u2f(0x7F000000u - (__float_as_uint(g) & 0x7F800000u));
+                                const float t = ex2(u2f(x[64 * hf + 8 * c + i]) - mu) * re;
+                                l4[i & 3] += t;
+                                p[i] = t * g;
+                            } else {
+                                p[i] = ex2(fmaf(u2f(x[64 * hf + 8 * c + i]), c2, -mu));
+                                l4[i & 3] += p[i];
+                            }
                         }
-                        // bf16 weights for the MMA; the sum keeps the float32 values, so the
+                        // bf16 (fp16) weights for the MMA; the sum keeps the float32 values, so the
                         // roundings (half a step, 2^-8 relative) average out in the output
                         *reinterpret_cast<uint4 *>(pl + sw128_offset(r, c)) =
-                            make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
-                                       pack_bf16(p[6], p[7]));
+                            kFp8 ? make_uint4(pack_f16(p[0], p[1]), pack_f16(p[2], p[3]), pack_f16(p[4], p[5]),
+                                              pack_f16(p[6], p[7]))
+                                 : make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
+                                              pack_bf16(p[6], p[7]));
                     }
                 }
                 l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
             }
             fence_proxy_async_smem();
+            if (kFp8) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->sig_free[slot]);
+            }
             // (the value CTA stages a piece's result in the P slots)
             if (kt < w.k0 + 2 && piece > 0 && !mbar_wait_cluster(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
@@ -779,21 +1059,24 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         // row statistics to the value CTA, the odd tiles' sum joined to the even tiles'
         // (a piece's result is out before the next piece's first P: see out_done)
         if (group == 1) {
-            sm->q.m_odd[r] = m;
-            sm->q.l_odd[r] = l;
+            // the piece's last maximum, if the other group's tile had it
+            if (((tile - 1) & 1) == 0 &&
+                !mbar_wait(&sm->m_bar[0][quad], ((tile - 1) >> 1) & 1, a.p.status, &sm->abort))
+                break;
+            const float mf = sm->q.m_run[r];
+            sm->q.l_odd[r] = m != -INFINITY ? l * ex2(m - mf) : 0.f;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->l_bar[quad]);
             if (!mbar_wait(&sm->l_read[quad], piece & 1, a.p.status, &sm->abort)) break;
         } else {
             if (!mbar_wait(&sm->l_bar[quad], piece & 1, a.p.status, &sm->abort)) break;
-            const float mo = sm->q.m_odd[r], lo = sm->q.l_odd[r];
+            const float mf = sm->q.m_run[r], lo = sm->q.l_odd[r];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->l_read[quad]);
-            const float mf = fmaxf(m, mo);  // (the later tile's: running maxima do not fall)
-            if (mf != -INFINITY) l = l * ex2(m - mf) + lo * ex2(mo - mf);
+            l = (m != -INFINITY ? l * ex2(m - mf) : 0.f) + lo;
             if (piece > 0 && !mbar_wait_cluster(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) break;
             if (live) {
-                st_remote(r_m + r * 4, __float_as_uint(mf), r_stat);
+                st_remote(r_m + r * 4, __float_as_uint(kFp8 ? mf - kShiftFp8 : mf), r_stat);
                 st_remote(r_l + r * 4, __float_as_uint(l), r_stat);
             }
             __syncwarp();
@@ -834,6 +1117,56 @@ __device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const 
         mbar_wait(&sm->v_full[i % kVStages], (i / kVStages) & 1, a.p.status, nullptr);
 }
 
+// Packed FP8 rows: units of 32 keys x 512 codes.
+__device__ void value_producer_fp8(const TcArgs &a, Small *sm, uint8_t *raw_sm, const CUtensorMap *mv) {
+    const int lane = threadIdx.x & 31;
+    const int box = min(a.box, 32), boxes = 32 / box;  // per unit, 1..4
+    uint32_t it = 0;
+    bool ok = true;
+    for (Walk w(a, sm); ok && w.valid(); w.next()) {
+        Box x = {a.p.n_pages, 0, false};
+        if (lane < 4 * boxes) x = find_box(a, w.s, w.b, w.k0 * kKeys + lane * box);
+        for (int kt = w.k0; ok && kt < w.k1; ++kt) {
+            const int units = (w.keys(kt) + 31) / 32;
+            for (int u = 0; u < units; ++u, ++it) {
+                const int st = it % kRawStages;
+                if (it >= kRawStages && !mbar_wait(&sm->v_free[st], (it / kRawStages - 1) & 1, a.p.status, &sm->abort)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&sm->v_full[st], kRawStage);
+                __syncwarp();
+                const int i = lane - u * boxes;
+                if (i >= 0 && i < boxes) tma_load_rows(raw_sm + st * kRawStage + i * box * 512, mv, &sm->v_full[st], 0, x);
+            }
+            if (kt + 1 < w.k1 && lane < 4 * boxes) x = find_box(a, w.s, w.b, (kt + 1) * kKeys + lane * box);
+        }
+    }
+    __syncwarp();
+    for (uint32_t i = it > kRawStages ? it - kRawStages : 0; i < it; ++i)
+        mbar_wait(&sm->v_full[i % kRawStages], (i / kRawStages) & 1, a.p.status, nullptr);
+}
+
+// One unit's codes to fp16 (exact), this warp's eighth: raw [4 groups of 8 keys][4 x
+// 128 dims][8 keys][128 bytes], widened [4][8 x 64 dims][8][128], both 128-byte
+// swizzled.  Eight lanes take the eight keys of a group, so neither side conflicts.
+// Rows from `live` on are past the sequence and may hold anything: zeros.
+__device__ __forceinline__ void widen_unit(const uint8_t *raw, uint8_t *h, int warp, int lane, int live) {
+    const int k = lane & 7;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int q = warp * 4 + (lane >> 3), c = q & 7, j = q >> 3;
+        uint4 v = *reinterpret_cast<const uint4 *>(raw + g * 4096 + j * 1024 + k * 128 + ((c ^ k) << 4));
+        if (8 * g + k >= live) v = make_uint4(0, 0, 0, 0);
+        uint8_t *d = h + g * 8192 + (2 * j + (c >> 2)) * 1024 + k * 128;
+        const int p = 2 * (c & 3);
+        *reinterpret_cast<uint4 *>(d + ((p ^ k) << 4)) =
+            make_uint4(widen2(v.x & 0xffffu), widen2(v.x >> 16), widen2(v.y & 0xffffu), widen2(v.y >> 16));
+        *reinterpret_cast<uint4 *>(d + (((p + 1) ^ k) << 4)) =
+            make_uint4(widen2(v.z & 0xffffu), widen2(v.z >> 16), widen2(v.w & 0xffffu), widen2(v.w >> 16));
+    }
+}
+
 // Posts a command to the output warps; they start once this thread's MMAs have
 // completed (the commit) and it has written the command (its own arrival).
 __device__ __forceinline__ bool post_command(const TcArgs &a, Small *sm, int cmd, uint32_t &phase, bool wait) {
@@ -845,6 +1178,7 @@ __device__ __forceinline__ bool post_command(const TcArgs &a, Small *sm, int cmd
     return !wait || mbar_wait(&sm->cmd_done, ph, a.p.status, &sm->abort);
 }
 
+template <bool kFp8>
 __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_sm) {
     const int lane = threadIdx.x & 31;
     const uint32_t tb = sm->tmem_base;
@@ -874,7 +1208,31 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
                 }
                 tc_fence_after();
             }
-            for (int g = 0; g < 2 * khs; ++g, ++it) {
+            if (kFp8) {
+                const int units = (w.keys(kt) + 31) / 32;
+                for (int u = 0; u < units; ++u, ++it) {
+                    const int st = it % kHStages;
+                    if (!mbar_wait(&sm->h_full[st], (it / kHStages) & 1, a.p.status, &sm->abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        tc_fence_after();
+                        const uint64_t hd = sdesc_sw128(smem_u32(v_sm), 1024, 8192);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int d = e >> 1, k = e & 1;  // dims 256 d .., keys 16 k ..
+                            umma_bf16(tb + 256 * d,
+                                      pd + static_cast<uint64_t>((slot * kPSlot + (u >> 1) * 2 * kBlk + (u & 1) * 64 + k * 32) >> 4),
+                                      hd + static_cast<uint64_t>((st * kHStage + d * 4096 + k * 16384) >> 4), kIdescO16,
+                                      (kt > w.k0 || u + k > 0) ? 1u : 0u);
+                        }
+                        umma_commit(&sm->h_free[st]);
+                    }
+                    __syncwarp();
+                }
+            }
+            for (int g = 0; !kFp8 && g < 2 * khs; ++g, ++it) {
                 const int d = g / khs, kh = g % khs, st = it % kVStages;
                 if (!mbar_wait(&sm->v_full[st], (it / kVStages) & 1, a.p.status, &sm->abort)) {
                     ok = false;
@@ -942,15 +1300,65 @@ __device__ __forceinline__ void put_rows(uint8_t *dst, int pitch, const uint8_t 
 }
 
 // Warp w: rows 32 (w & 3) + lane, output dims 256 (w >> 2) .. + 255.
-__device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, int cluster) {
+// Packed FP8 rows: between commands the warps widen the codes.
+template <bool kFp8>
+__device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const uint8_t *raw_sm, uint8_t *h_sm, int cluster) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
     const int r = 32 * quad + lane;
     const uint32_t tb = sm->tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + 256 * half;
     const uint32_t r_done = map_rank(smem_u32(&sm->out_done), 0);
     uint32_t cphase = 0, piece = 0;
     Walk w(a, sm);
+    Walk cw(a, sm);  // the units being widened
+    int ckt = cw.k0, cu = 0;
+    uint32_t cit = 0, idle = 0;
+    uint64_t t_idle = 0;
     while (true) {
-        if (!mbar_wait(&sm->cmd_full, cphase, a.p.status, &sm->abort)) break;
+        if (kFp8) {
+            // whichever is ready: a unit to widen, or a command; neither waits for the other
+            // (a finished piece's output comes while the next one's units already wait)
+            bool can = cw.valid();
+            if (can) {
+                const uint32_t rs = cit % kRawStages, hs = cit % kHStages;
+                can = (cit < kHStages || mbar_test_wait(&sm->h_free[hs], (cit / kHStages - 1) & 1)) &&
+                      mbar_test_wait(&sm->v_full[rs], (cit / kRawStages) & 1);
+                if (__all_sync(0xffffffffu, can)) {
+                    widen_unit(raw_sm + rs * kRawStage, h_sm + hs * kHStage, warp, lane, cw.s.len - ckt * kKeys - 32 * cu);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm->v_free[rs]);
+                        mbar_arrive(&sm->h_full[hs]);
+                    }
+                    ++cit;
+                    if (++cu == (cw.keys(ckt) + 31) / 32) {
+                        cu = 0;
+                        if (++ckt == cw.k1) {
+                            cw.next();
+                            ckt = cw.k0;
+                        }
+                    }
+                    idle = 0;
+                    continue;
+                }
+            }
+            if (!__all_sync(0xffffffffu, mbar_test_wait(&sm->cmd_full, cphase))) {
+                if ((++idle & 255u) == 0) {
+                    if (*reinterpret_cast<volatile int *>(&sm->abort)) break;
+                    const uint64_t now = global_timer_ns();
+                    if (idle == 256) t_idle = now;
+                    if (now - t_idle > kWaitLimitNs) {
+                        report_status(a.p.status, DSA_ERR_TIMEOUT);
+                        sm->abort = 1;
+                        break;
+                    }
+                }
+                continue;
+            }
+            idle = 0;
+        } else if (!mbar_wait(&sm->cmd_full, cphase, a.p.status, &sm->abort)) {
+            break;
+        }
         cphase ^= 1;
         tc_fence_after();
         const int cmd = *reinterpret_cast<volatile int *>(&sm->cmd);
@@ -1054,9 +1462,14 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, int clu
     }
 }
 
+struct TcMaps {
+    CUtensorMap q, k, v;  // queries; cache rows for either product
+    CUtensorMap q8, r;    // packed FP8 rows: the queries' two terms, the RoPE keys
+};
+
+template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    paged_mla_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                        const __grid_constant__ CUtensorMap mv) {
+    paged_mla_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Small *sm = reinterpret_cast<Small *>(smem + kBig);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1070,7 +1483,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&sm->v_full[i], 1);
-            mbar_init(&sm->v_free[i], 1);
+            mbar_init(&sm->v_free[i], kFp8 ? 8 : 1);
+        }
+        for (int i = 0; i < kHStages; ++i) {
+            mbar_init(&sm->h_full[i], 8);
+            mbar_init(&sm->h_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->sig_full[i], 1);
+            mbar_init(&sm->sig_free[i], 4);
         }
         for (int i = 0; i < kSBufs; ++i) {
             mbar_init(&sm->s_full[i], 1);
@@ -1100,9 +1521,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     if (warp == 8 && lane == 0) {
-        tma_prefetch_desc(&mq);
-        tma_prefetch_desc(&mk);
-        tma_prefetch_desc(&mv);
+        tma_prefetch_desc(&maps.q);
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+        if (kFp8) {
+            tma_prefetch_desc(&maps.q8);
+            tma_prefetch_desc(&maps.r);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -1122,19 +1547,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     else
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (rank == 0) {
-        if (warp < 8)
-            score_softmax(a, sm, smem + kQBytes, map_rank(smem_u32(smem), 1));
-        else if (warp == 8)
-            score_producer(a, sm, smem, smem + kQBytes, smem + kQBytes + 2 * kPSlot, &mq, &mk);
-        else if (warp == 9 && lane == 0)
-            score_mma(a, sm, smem, smem + kQBytes, smem + kQBytes + 2 * kPSlot);
+        uint8_t *stage = smem + kQBytes, *ring = stage + 2 * kPSlot;
+        if (warp < 8) {
+            score_softmax<kFp8>(a, sm, stage, map_rank(smem_u32(smem), 1));
+        } else if (kFp8) {
+            if (warp == 8)
+                score_producer_fp8(a, sm, smem, stage, ring, ring + 2 * kCodes, &maps.q, &maps.q8, &maps.k, &maps.r);
+            else if (warp == 9 && lane == 0)
+                score_mma_fp8(a, sm, smem, stage, ring, ring + 2 * kCodes);
+            else if (warp == 10)
+                score_scales_fp8(a, sm);
+        } else if (warp == 8) {
+            score_producer(a, sm, smem, stage, ring, &maps.q, &maps.k);
+        } else if (warp == 9 && lane == 0) {
+            score_mma(a, sm, smem, stage, ring);
+        }
     } else {
+        uint8_t *v_sm = smem + 2 * kPSlot, *h_sm = v_sm + kRawStages * kRawStage;
         if (warp < 8)
-            value_output(a, sm, smem, cluster);
+            value_output<kFp8>(a, sm, smem, v_sm, h_sm, cluster);
+        else if (warp == 8 && kFp8)
+            value_producer_fp8(a, sm, v_sm, &maps.v);
         else if (warp == 8)
-            value_producer(a, sm, smem + 2 * kPSlot, &mv);
+            value_producer(a, sm, v_sm, &maps.v);
         else if (warp == 9)
-            value_mma(a, sm, smem, smem + 2 * kPSlot);
+            value_mma<kFp8>(a, sm, smem, kFp8 ? h_sm : v_sm);
     }
     __syncwarp();
     griddep_launch_dependents();
@@ -1144,6 +1581,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(sm->tmem_base, 512);
     }
+}
+
+// The latent part of each query row (token, head) as s (q1 + q2): s a power of two
+// that brings the row's largest value under E4M3's 448, q1 the nearest E4M3 value, q2
+// the nearest to what is left (exact but below 2^-18 of the row's largest value).
+// One warp per row, 16 dims per lane; bound by launch latency at decode sizes.
+__global__ void __launch_bounds__(256) split_queries_kernel(const __nv_bfloat16 *q, uint8_t *q8, float *scale, int64_t rows) {
+    griddep_wait();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const uint4 *src = reinterpret_cast<const uint4 *>(q + row * kRow + 16 * lane);
+    const uint4 in[2] = {src[0], src[1]};
+    float v[16];
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t two = reinterpret_cast<const uint32_t *>(in)[i];
+        v[2 * i] = u2f(two << 16);
+        v[2 * i + 1] = u2f(two & 0xFFFF0000u);
+        mx = fmaxf(mx, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // 2^k with mx 2^-k in (224, 448] (k kept where both powers are normal numbers)
+    const uint32_t bits = __float_as_uint(mx);
+    int k = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    k = mx > 0.f ? min(max(k, -120), 120) : 0;
+    const float down = u2f(static_cast<uint32_t>(127 - k) << 23);
+    uint32_t t1[4], t2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        t1[i] = t2[i] = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 x = make_float2(v[4 * i + 2 * h] * down, v[4 * i + 2 * h + 1] * down);
+            const uint32_t c1 = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+            const uint32_t w = widen2(c1);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+            const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(x.x - f.x, x.y - f.y), __NV_SATFINITE, __NV_E4M3);
+            t1[i] |= c1 << (16 * h);
+            t2[i] |= c2 << (16 * h);
+        }
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(q8 + row * 2 * kLatent + 16 * lane);
+    dst[0] = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+    dst[kLatent / 16] = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+    if (lane == 0) scale[row] = u2f(static_cast<uint32_t>(127 + k) << 23);
 }
 
 // Merge of the row tiles that a cut divided: o = sum_i 2^(m_i - M) o_i / sum_i
@@ -1215,57 +1700,91 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 bool paged_mla_tc_shape(const PagedMlaArgs &a) {
     // (the softmax takes the maximum before it scales: a positive scale)
-    if (!a.is_bf16 || a.kv_fp8 || !(a.scale > 0.f) || a.scale > FLT_MAX || a.heads > kRows || a.d_lat != kLatent || a.d_rope != kRope) return false;
-    if (a.page_rows % 8 != 0 || a.kv_row_stride % 8 != 0 || a.kv_row_stride < kRow) return false;
-    if (a.kv_page_stride % 8 != 0 || a.kv_page_stride < 1) return false;
+    if (!a.is_bf16 || !(a.scale > 0.f) || a.scale > FLT_MAX || a.heads > kRows || a.d_lat != kLatent || a.d_rope != kRope)
+        return false;
+    const int64_t unit = a.kv_fp8 ? 16 : 8, row = a.kv_fp8 ? kFp8Row : kRow;
+    if (a.page_rows % 8 != 0 || a.kv_row_stride % unit != 0 || a.kv_row_stride < row) return false;
+    if (a.kv_page_stride % unit != 0 || a.kv_page_stride < 1) return false;
     const auto mis = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.kv) | reinterpret_cast<uintptr_t>(a.out);
     return (mis & 15u) == 0 && static_cast<int64_t>(a.n_tok) * a.heads < INT32_MAX;
 }
 
-size_t paged_mla_tc_scratch(int num_sms) {
-    const size_t c = std::min(num_sms / 2, kMaxParts);
-    return align256(c * sizeof(Meta)) + align256(2 * c * kRows * 2 * sizeof(float)) + 2 * c * kRows * kLatent * sizeof(float);
+static int tc_clusters(int num_sms) { return std::min(num_sms / 2, kMaxParts); }
+
+size_t paged_mla_tc_scratch(const PagedMlaArgs &p, int num_sms) {
+    const size_t c = tc_clusters(num_sms), rows = p.kv_fp8 ? static_cast<size_t>(p.n_tok) * p.heads : 0;
+    return align256(c * sizeof(Meta)) + align256(2 * c * kRows * 2 * sizeof(float)) +
+           2 * c * kRows * kLatent * sizeof(float) + rows * 2 * kLatent + rows * sizeof(float);
 }
 
 cudaError_t launch_paged_mla_tc(const PagedMlaArgs &p, void *scratch, int num_sms, cudaStream_t st) {
     EncodeTiledFn enc = tma_encode_fn();
     if (!enc) return cudaErrorNotSupported;
-    TcArgs a;
+    TcArgs a = {};
     a.p = p;
-    a.clusters = std::min(num_sms / 2, kMaxParts);
+    a.clusters = tc_clusters(num_sms);
     a.tok_tile = kRows / p.heads;
     a.box = 64;
     while (p.page_rows % a.box != 0) a.box >>= 1;
+    const int64_t rows = static_cast<int64_t>(p.n_tok) * p.heads;
     uint8_t *s = static_cast<uint8_t *>(scratch);
     a.meta = reinterpret_cast<Meta *>(s);
     s += align256(a.clusters * sizeof(Meta));
     a.part_ml = reinterpret_cast<float *>(s);
     s += align256(static_cast<size_t>(2) * a.clusters * kRows * 2 * sizeof(float));
     a.part_o = reinterpret_cast<float *>(s);
-    CUtensorMap mq, mk, mv;
-    const cuuint32_t es[2] = {1, 1};
-    const cuuint64_t qd[2] = {static_cast<cuuint64_t>(kRow), static_cast<cuuint64_t>(p.n_tok) * p.heads};
+    s += static_cast<size_t>(2) * a.clusters * kRows * kLatent * sizeof(float);
+    uint8_t *q8 = s;
+    float *q8_scale = reinterpret_cast<float *>(s + rows * 2 * kLatent);
+    a.q8 = q8;
+    a.q8_scale = q8_scale;
+    TcMaps m = {};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    auto encode = [&](CUtensorMap *map, CUtensorMapDataType dt, cuuint32_t rank, const void *base, const cuuint64_t *dims,
+                      const cuuint64_t *strides, const cuuint32_t *box) {
+        return enc(map, dt, rank, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+               CUDA_SUCCESS;
+    };
+    const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const cuuint64_t qd[2] = {static_cast<cuuint64_t>(kRow), static_cast<cuuint64_t>(rows)};
     const cuuint64_t qs[1] = {static_cast<cuuint64_t>(kRow) * 2};
     const cuuint32_t qb[2] = {64, 64};
-    if (enc(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p.q), qd, qs, qb, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    // cache rows: {64 dims, 8 rows, 9 blocks, groups of a page, pages}
-    const cuuint32_t es5[5] = {1, 1, 1, 1, 1};
-    const cuuint64_t kd[5] = {64, 8, kNB, static_cast<cuuint64_t>(p.page_rows / 8), static_cast<cuuint64_t>(p.n_pages)};
-    const cuuint64_t rs = static_cast<cuuint64_t>(p.kv_row_stride) * 2;
-    const cuuint64_t ks[4] = {rs, 128, 8 * rs, static_cast<cuuint64_t>(p.kv_page_stride) * 2};
-    const cuuint32_t kb[5] = {64, 8, kKBlocks, static_cast<cuuint32_t>(a.box / 8), 1};
-    const cuuint32_t vb[5] = {64, 8, 4, static_cast<cuuint32_t>(a.box / 8), 1};
-    for (int i = 0; i < 2; ++i)
-        if (enc(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(p.kv), kd, ks, i ? vb : kb, es5,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
-    cudaError_t e = set_max_dynamic_smem(paged_mla_tc_kernel, kBig + static_cast<int>(sizeof(Small)));
+    bool ok = encode(&m.q, bf, 2, p.q, qd, qs, qb);
+    const cuuint64_t groups = static_cast<cuuint64_t>(p.page_rows / 8), pages = static_cast<cuuint64_t>(p.n_pages);
+    const cuuint32_t g64 = static_cast<cuuint32_t>(a.box / 8), g32 = std::min<cuuint32_t>(g64, 4);
+    if (!p.kv_fp8) {
+        // cache rows: {64 dims, 8 rows, 9 blocks, groups of a page, pages}
+        const cuuint64_t rs = static_cast<cuuint64_t>(p.kv_row_stride) * 2;
+        const cuuint64_t kd[5] = {64, 8, kNB, groups, pages};
+        const cuuint64_t ks[4] = {rs, 128, 8 * rs, static_cast<cuuint64_t>(p.kv_page_stride) * 2};
+        const cuuint32_t kb[5] = {64, 8, kKBlocks, g64, 1}, vb[5] = {64, 8, 4, g64, 1};
+        ok = ok && encode(&m.k, bf, 5, p.kv, kd, ks, kb) && encode(&m.v, bf, 5, p.kv, kd, ks, vb);
+    } else {
+        // codes: {128 dims, 8 rows, 4 blocks, groups, pages}; RoPE keys: {64 dims, 8 rows, groups, pages}
+        const cuuint64_t rs = static_cast<cuuint64_t>(p.kv_row_stride), ps = static_cast<cuuint64_t>(p.kv_page_stride);
+        const cuuint64_t kd[5] = {128, 8, 4, groups, pages}, ks[4] = {rs, 128, 8 * rs, ps};
+        const cuuint32_t kb[5] = {128, 8, 4, g64, 1}, vb[5] = {128, 8, 4, g32, 1};
+        const cuuint64_t rd[4] = {64, 8, groups, pages}, rst[3] = {rs, 8 * rs, ps};
+        const cuuint32_t rb[4] = {64, 8, g64, 1};
+        const cuuint64_t q8d[2] = {2 * kLatent, static_cast<cuuint64_t>(rows)}, q8s[1] = {2 * kLatent};
+        const cuuint32_t q8b[2] = {128, 64};
+        ok = ok && encode(&m.k, u8, 5, p.kv, kd, ks, kb) && encode(&m.v, u8, 5, p.kv, kd, ks, vb) &&
+             encode(&m.r, bf, 4, static_cast<const uint8_t *>(p.kv) + kFp8RopeOff, rd, rst, rb) &&
+             encode(&m.q8, u8, 2, q8, q8d, q8s, q8b);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    cudaError_t e = cudaSuccess;
+    if (p.kv_fp8) {
+        e = launch_pdl(split_queries_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st,
+                       static_cast<const __nv_bfloat16 *>(p.q), q8, q8_scale, rows);
+        if (e != cudaSuccess) return e;
+    }
+    auto kernel = p.kv_fp8 ? paged_mla_tc_kernel<true> : paged_mla_tc_kernel<false>;
+    const int smem = kBig + static_cast<int>(sizeof(Small));
+    e = set_max_dynamic_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(paged_mla_tc_kernel, dim3(2 * a.clusters), dim3(kThreads), kBig + sizeof(Small), st, a, mq, mk, mv);
+    e = launch_pdl(kernel, dim3(2 * a.clusters), dim3(kThreads), smem, st, a, m);
     if (e != cudaSuccess) return e;
     return launch_pdl(paged_mla_merge_kernel, dim3(a.clusters, kRows / kMergeRows), dim3(128 * kMergeRows), 0, st, a);
 }
