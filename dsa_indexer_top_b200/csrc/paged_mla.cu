@@ -117,6 +117,7 @@ struct Small {
     uint64_t fin;
     // packed FP8 rows
     uint64_t sig_full[2], sig_free[2];                // score CTA: row scales of the tiles of either parity
+    int sig_exp[2], sig_gap[2];                       // .. their power of two; some key of the tile has none
     uint64_t h_full[kHStages], h_free[kHStages];      // value CTA: widened units
     uint32_t tmem_base;
     int abort;
@@ -786,7 +787,8 @@ __device__ void score_producer_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, ui
     if (q_use > 0) mbar_wait(&sm->q_full, (q_use - 1) & 1, a.p.status, nullptr);
 }
 
-// Row scales of every key tile to shared memory, 0 for a row nobody sees.
+// Row scales of every key tile to shared memory, divided by the tile's largest power
+// of two; 0 for a row nobody sees.
 __device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
     const int lane = threadIdx.x & 31;
     uint32_t tile = 0;
@@ -802,8 +804,20 @@ __device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
                 for (int i = 0; i < 4; ++i)
                     if (s0 + i < w.s.len) v[i] = __ldg(reinterpret_cast<const float *>(row + i * a.p.kv_row_stride));
             }
+            float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+            const bool gap = __any_sync(0xffffffffu, !(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])) > 0.f));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+            e = mx > 0.f ? min(max(e, -120), 120) : 0;
+            const float down = u2f(static_cast<uint32_t>(127 - e) << 23);
             if (tile >= 2 && !mbar_wait(&sm->sig_free[tile & 1], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) return;
-            *reinterpret_cast<float4 *>(&sm->q.sigma[tile & 1][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(&sm->q.sigma[tile & 1][4 * lane]) =
+                make_float4(v[0] * down, v[1] * down, v[2] * down, v[3] * down);
+            if (lane == 0) {
+                sm->sig_exp[tile & 1] = e;
+                sm->sig_gap[tile & 1] = gap;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->sig_full[tile & 1]);
         }
@@ -917,6 +931,10 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             const uint32_t okbits = kFp8 ? 0xFFFFu : *reinterpret_cast<volatile uint32_t *>(&sm->key_ok[slot]);
             const float *sig = sm->q.sigma[slot];
             const int nk = w.keys(kt);
+            // packed FP8 rows: the tile's row scales are 2^sig_exp times what is in sig
+            const float te = kFp8 ? static_cast<float>(*reinterpret_cast<volatile int *>(&sm->sig_exp[slot])) : 0.f;
+            const float qs = kFp8 ? qc2 * ex2(te) : 0.f;
+            const bool gap = kFp8 ? *reinterpret_cast<volatile int *>(&sm->sig_gap[slot]) != 0 : okbits != 0xFFFFu;
             uint32_t x[128];
             if (live && !kFp8) {
 #pragma unroll
@@ -925,8 +943,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                 tmem_ld_wait();
             }
             if (live && kFp8) {
-                // log2 of weight times 2^e, the row scale's power of two, which bounds what the
-                // MMA gets: c2 (s sigma S_lat + S_rope) + e
+                // log2 of the weight: c2 (s sigma S_lat + S_rope)
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
                     uint32_t y[32];
@@ -938,12 +955,8 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                         const float4 g4 = *reinterpret_cast<const float4 *>(sig + c + i);
                         const float g[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            // exponent as a float: its biased value in the low bits of 2^23
-                            const float e = u2f(0x4B000000u | (__float_as_uint(g[k]) >> 23)) - (8388608.f + 127.f);
-                            const float t = fmaf(u2f(x[c + i + k]) * g[k], qc2, fmaf(u2f(y[i + k]), c2, e));
-                            x[c + i + k] = g[k] > 0.f ? __float_as_uint(t) : 0xFF800000u;
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            x[c + i + k] = __float_as_uint(fmaf(u2f(x[c + i + k]) * g[k], qs, u2f(y[i + k]) * c2));
                     }
                 }
             }
@@ -953,10 +966,10 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             float mx = -INFINITY;
             if (live) {
                 const int s0 = kt * kKeys;
-                if (s0 + kKeys - 1 > pos0 || okbits != 0xFFFFu) {
+                if (s0 + kKeys - 1 > pos0 || gap) {
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
-                        if (s0 + i > pos || !((okbits >> (i / 8)) & 1)) x[i] = 0xFF800000u;
+                        if (s0 + i > pos || (kFp8 ? !(sig[i] > 0.f) : !((okbits >> (i / 8)) & 1))) x[i] = 0xFF800000u;
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -964,7 +977,9 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
 #pragma unroll
                     for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], u2f(x[i + k]));
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                if (!kFp8) mx *= c2;  // (scale > 0)
+                // (the running maximum is of the weight times the tile's power of two, which
+                // bounds what the MMA gets)
+                mx = kFp8 ? mx + te : mx * c2;  // (scale > 0)
             }
             // the previous tile's running maximum
             float mp = -INFINITY;
@@ -994,8 +1009,8 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                 break;
             }
             if (live) {
-                const float mu = (m == -INFINITY ? 0.f : m) - (kFp8 ? kShiftFp8 : 0.f);
-                float l4[4] = {l, 0.f, 0.f, 0.f};
+                const float mu = (m == -INFINITY ? 0.f : m) - (kFp8 ? kShiftFp8 + te : 0.f);
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     if (hf && nk <= 64) break;
@@ -1006,12 +1021,9 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             if (kFp8) {
-                                // weight = 2^x / 2^e; the codes' weight has the whole scale
-                                const float g = sig[64 * hf + 8 * c + i];
-                                const float re = u2f(0x7F000000u - (__float_as_uint(g) & 0x7F800000u));
-                                const float t = ex2(u2f(x[64 * hf + 8 * c + i]) - mu) * re;
+                                const float t = ex2(u2f(x[64 * hf + 8 * c + i]) - mu);
                                 l4[i & 3] += t;
-                                p[i] = t * g;
+                                p[i] = t * sig[64 * hf + 8 * c + i];
                             } else {
                                 p[i] = ex2(fmaf(u2f(x[64 * hf + 8 * c + i]), c2, -mu));
                                 l4[i & 3] += p[i];
@@ -1026,7 +1038,8 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                                               pack_bf16(p[6], p[7]));
                     }
                 }
-                l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                const float lt = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                l += kFp8 ? lt * ex2(-te) : lt;
             }
             fence_proxy_async_smem();
             if (kFp8) {
@@ -1147,15 +1160,15 @@ __device__ void value_producer_fp8(const TcArgs &a, Small *sm, uint8_t *raw_sm, 
         mbar_wait(&sm->v_full[i % kRawStages], (i / kRawStages) & 1, a.p.status, nullptr);
 }
 
-// One unit's codes to fp16 (exact), this warp's eighth: raw [4 groups of 8 keys][4 x
+// One unit's codes to fp16 (exact), this warp's quarter (of four): raw [4 groups of 8 keys][4 x
 // 128 dims][8 keys][128 bytes], widened [4][8 x 64 dims][8][128], both 128-byte
 // swizzled.  Eight lanes take the eight keys of a group, so neither side conflicts.
 // Rows from `live` on are past the sequence and may hold anything: zeros.
 __device__ __forceinline__ void widen_unit(const uint8_t *raw, uint8_t *h, int warp, int lane, int live) {
     const int k = lane & 7;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int q = warp * 4 + (lane >> 3), c = q & 7, j = q >> 3;
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i) {
+        const int q = (i & 1) * 16 + warp * 4 + (lane >> 3), c = q & 7, j = q >> 3, g = i >> 1;
         uint4 v = *reinterpret_cast<const uint4 *>(raw + g * 4096 + j * 1024 + k * 128 + ((c ^ k) << 4));
         if (8 * g + k >= live) v = make_uint4(0, 0, 0, 0);
         uint8_t *d = h + g * 8192 + (2 * j + (c >> 2)) * 1024 + k * 128;
@@ -1319,16 +1332,20 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
             // (a finished piece's output comes while the next one's units already wait)
             bool can = cw.valid();
             if (can) {
+                // warps 0-3 take the even units, 4-7 the odd ones
                 const uint32_t rs = cit % kRawStages, hs = cit % kHStages;
-                can = (cit < kHStages || mbar_test_wait(&sm->h_free[hs], (cit / kHStages - 1) & 1)) &&
-                      mbar_test_wait(&sm->v_full[rs], (cit / kRawStages) & 1);
+                const bool mine = (cit & 1) == static_cast<uint32_t>(half);
+                can = !mine || ((cit < kHStages || mbar_test_wait(&sm->h_free[hs], (cit / kHStages - 1) & 1)) &&
+                       mbar_test_wait(&sm->v_full[rs], (cit / kRawStages) & 1));
                 if (__all_sync(0xffffffffu, can)) {
-                    widen_unit(raw_sm + rs * kRawStage, h_sm + hs * kHStage, warp, lane, cw.s.len - ckt * kKeys - 32 * cu);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sm->v_free[rs]);
-                        mbar_arrive(&sm->h_full[hs]);
+                    if (mine) {
+                        widen_unit(raw_sm + rs * kRawStage, h_sm + hs * kHStage, quad, lane, cw.s.len - ckt * kKeys - 32 * cu);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&sm->v_free[rs]);
+                            mbar_arrive(&sm->h_full[hs]);
+                        }
                     }
                     ++cit;
                     if (++cu == (cw.keys(ckt) + 31) / 32) {
@@ -1483,10 +1500,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&sm->v_full[i], 1);
-            mbar_init(&sm->v_free[i], kFp8 ? 8 : 1);
+            mbar_init(&sm->v_free[i], kFp8 ? 4 : 1);
         }
         for (int i = 0; i < kHStages; ++i) {
-            mbar_init(&sm->h_full[i], 8);
+            mbar_init(&sm->h_full[i], 4);
             mbar_init(&sm->h_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
