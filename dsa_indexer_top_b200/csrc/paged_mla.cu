@@ -106,9 +106,7 @@ struct Box {  // a TMA copy of cache rows: page and 8-row group in it
 struct Small {
     // score CTA
     uint64_t q_full, q_free, k_full[kKStages], k_free[kKStages], s_full[kSBufs], s_free[kSBufs];
-    uint64_t m_bar[2][4];     // [tile parity][quadrant]: the tile's running maxima are in m_run
-    uint64_t l_bar[4];        // the odd tiles' sums are in
-    uint64_t l_read[4];       // .. and have been read: both groups leave a piece together
+    uint64_t x_bar[4];        // the two warps of a quadrant have written their maxima
     uint64_t p_free[2];       // P V of the slot's tile has completed (from the value CTA)
     uint64_t p_got[2];        // the slot's tile has arrived there
     uint64_t out_done;        // the value CTA has written a piece's result (its P slots are free)
@@ -130,7 +128,8 @@ struct Small {
     uint32_t key_ok[kSBufs];  // score CTA: [S buffer] bit i: keys 8i..8i+7 are in the pool
     union {
         struct alignas(16) {  // (the scales are read 16 bytes at a time)
-            float m_run[kRows], l_odd[kRows], sigma[2][kKeys];  // score CTA
+            float sigma[2][kKeys];      // score CTA: [tile parity] row scales
+            uint16_t xmax[2][2][kRows];  // [tile parity][half][row] maxima, bf16
         } q;
         struct {
             float alpha[2][kRows];  // value CTA: [slot][row]
@@ -893,21 +892,29 @@ __device__ void score_mma_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t
     mbar_wait(&sm->fin, 0, a.p.status, nullptr);
 }
 
-// Softmax.  Warps 0-3 take the even tiles, 4-7 the odd ones, so that one tile's
-// exponentials run beside the next one's loads and exchanges; thread r of a group
-// holds row r's 128 logits.  The running maxima pass from tile to tile through
-// shared memory; each group keeps the sum of its own tiles, relative to the maximum
-// it saw last.
+// Softmax.  Warp w: rows 32 (w & 3) + lane, keys 64 (w >> 2) .. + 63 of every tile;
+// the two warps of a quadrant exchange their maxima (as bf16, rounded up: any
+// reference not far below the maximum will do, as long as both take the same).  A
+// loop body that fits the instruction cache matters more than anything else here: a
+// thread per row with 128 logits in registers, its loops unrolled, waited for
+// instructions more often than it issued one.
+__device__ __forceinline__ float bf16_up(float x) {
+    // the next bf16 at or above x (x finite or -infinity)
+    const uint32_t b = __float_as_uint(x);
+    const uint32_t t = b & 0xFFFF0000u;
+    return u2f((b & 0xFFFFu) && !(b >> 31) ? t + 0x10000u : t);
+}
+
 template <bool kFp8>
 __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint32_t p_remote) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, group = warp >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
     const int r = 32 * quad + lane;
-    const uint32_t tb = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t tb = (static_cast<uint32_t>(32 * quad) << 16) + 64 * half;
     const float c2 = a.p.scale * kLog2e;
     const uint32_t r_alpha = map_rank(smem_u32(&sm->v.alpha[0][0]), 1), r_flags = map_rank(smem_u32(&sm->flags[0][0]), 1);
     const uint32_t r_pfull = map_rank(smem_u32(&sm->p_full[0]), 1), r_stat = map_rank(smem_u32(&sm->stat_full), 1);
     const uint32_t r_m = map_rank(smem_u32(&sm->v.m[0]), 1), r_l = map_rank(smem_u32(&sm->v.l[0]), 1);
-    uint32_t tile = 0, piece = 0;
+    uint32_t tile = 0, piece = 0, xphase = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
         const int rows = w.rows();
@@ -919,44 +926,45 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         const float qc2 = kFp8 ? c2 * a.q8_scale[w.row0() + min(r, rows - 1)] : 0.f;
         float m = -INFINITY, l = 0.f;
         for (int kt = w.k0; kt < w.k1; ++kt, ++tile) {
-            const uint32_t slot = tile & 1;  // of P, and of the S buffers
-            const uint32_t sbuf = kFp8 ? 0 : slot;  // (its barrier of arrivals; s_full is by tile parity)
-            if (slot != static_cast<uint32_t>(group)) continue;
+            const uint32_t slot = tile & 1;  // of P, and of bf16's S buffers
+            const uint32_t sbuf = kFp8 ? 0 : slot;
             if ((kFp8 && !mbar_wait(&sm->sig_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) ||
                 !mbar_wait(&sm->s_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const uint32_t okbits = kFp8 ? 0xFFFFu : *reinterpret_cast<volatile uint32_t *>(&sm->key_ok[slot]);
-            const float *sig = sm->q.sigma[slot];
             const int nk = w.keys(kt);
+            const bool used = live && 64 * half < nk;
+            const float *sig = &sm->q.sigma[slot][64 * half];
+            const uint32_t okbits =
+                kFp8 ? 0xFFu : *reinterpret_cast<volatile uint32_t *>(&sm->key_ok[slot]) >> (8 * half) & 0xFFu;
             // packed FP8 rows: the tile's row scales are 2^sig_exp times what is in sig
             const float te = kFp8 ? static_cast<float>(*reinterpret_cast<volatile int *>(&sm->sig_exp[slot])) : 0.f;
-            const float qs = kFp8 ? qc2 * ex2(te) : 0.f;
-            const bool gap = kFp8 ? *reinterpret_cast<volatile int *>(&sm->sig_gap[slot]) != 0 : okbits != 0xFFFFu;
-            uint32_t x[128];
-            if (live && !kFp8) {
-#pragma unroll
-                for (int c = 0; c < 128; c += 32)
-                    tmem_ld32(tb + kKeys * slot + c, reinterpret_cast<uint32_t(&)[32]>(x[c]));
-                tmem_ld_wait();
-            }
-            if (live && kFp8) {
-                // log2 of the weight: c2 (s sigma S_lat + S_rope)
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t y[32];
-                    tmem_ld32(tb + c, reinterpret_cast<uint32_t(&)[32]>(x[c]));
-                    tmem_ld32(tb + kKeys + c, y);
+            const bool gap = kFp8 ? *reinterpret_cast<volatile int *>(&sm->sig_gap[slot]) != 0 : okbits != 0xFFu;
+            uint32_t x[64];
+            if (used) {
+                if constexpr (!kFp8) {
+                    tmem_ld32(tb + kKeys * slot, reinterpret_cast<uint32_t(&)[32]>(x[0]));
+                    tmem_ld32(tb + kKeys * slot + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
                     tmem_ld_wait();
+                } else {
+                    // log2 of the weight: c2 (s sigma S_lat + S_rope)
+                    const float qs = qc2 * ex2(te);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 g4 = *reinterpret_cast<const float4 *>(sig + c + i);
-                        const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t y[32];
+                        tmem_ld32(tb + c, reinterpret_cast<uint32_t(&)[32]>(x[c]));
+                        tmem_ld32(tb + kKeys + c, y);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            x[c + i + k] = __float_as_uint(fmaf(u2f(x[c + i + k]) * g[k], qs, u2f(y[i + k]) * c2));
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 g4 = *reinterpret_cast<const float4 *>(sig + c + i);
+                            const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[c + i + k] = __float_as_uint(fmaf(u2f(x[c + i + k]) * g[k], qs, u2f(y[i + k]) * c2));
+                        }
                     }
                 }
             }
@@ -964,79 +972,73 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->s_free[sbuf]);
             float mx = -INFINITY;
-            if (live) {
-                const int s0 = kt * kKeys;
-                if (s0 + kKeys - 1 > pos0 || gap) {
+            if (used) {
+                const int s0 = kt * kKeys + 64 * half;
+                if (s0 + 63 > pos0 || gap) {
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
+                    for (int i = 0; i < 64; ++i)
                         if (s0 + i > pos || (kFp8 ? !(sig[i] > 0.f) : !((okbits >> (i / 8)) & 1))) x[i] = 0xFF800000u;
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 128; i += 4)
+                for (int i = 0; i < 64; i += 4)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], u2f(x[i + k]));
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 // (the running maximum is of the weight times the tile's power of two, which
                 // bounds what the MMA gets)
-                mx = kFp8 ? mx + te : mx * c2;  // (scale > 0)
+                mx = bf16_up(kFp8 ? mx + te : mx * c2);  // (scale > 0)
             }
-            // the previous tile's running maximum
-            float mp = -INFINITY;
-            if (kt > w.k0) {
-                if (!mbar_wait(&sm->m_bar[slot ^ 1][quad], ((tile - 1) >> 1) & 1, a.p.status, &sm->abort)) {
+            float al = 1.f;
+            if (live) {
+                sm->q.xmax[slot][half][r] = static_cast<uint16_t>(__float_as_uint(mx) >> 16);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
+                if (!mbar_wait(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
-                mp = sm->q.m_run[r];
+                xphase ^= 1;
+                mx = fmaxf(mx, u2f(static_cast<uint32_t>(sm->q.xmax[slot][half ^ 1][r]) << 16));
+                if (m == -INFINITY) {
+                    m = mx;  // nothing accumulated for the row yet
+                } else if (r < rows && mx > m + (kFp8 ? kRescaleFp8 : kRescale)) {
+                    al = ex2(m - mx);
+                    m = mx;
+                    l *= al;
+                }
             }
-            float mn = mp, al = 1.f;
-            if (mp == -INFINITY) {
-                mn = mx;  // nothing accumulated for the row yet
-            } else if (r < rows && mx > mp + (kFp8 ? kRescaleFp8 : kRescale)) {
-                al = ex2(mp - mx);
-                mn = mx;
-            }
-            sm->q.m_run[r] = mn;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->m_bar[slot][quad]);
-            if (m != -INFINITY && m != mn) l *= ex2(m - mn);
-            m = mn;
             const bool flag = __any_sync(0xffffffffu, al != 1.f);
             // the staged tile two back has left
             if (tile >= 2 && !mbar_wait_cluster(&sm->p_got[slot], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
-            if (live) {
+            if (used) {
                 const float mu = (m == -INFINITY ? 0.f : m) - (kFp8 ? kShiftFp8 + te : 0.f);
                 float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                uint8_t *pl = p_stage + slot * kPSlot + half * 2 * kBlk;
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    if (hf && nk <= 64) break;
-                    uint8_t *pl = p_stage + slot * kPSlot + hf * 2 * kBlk;
+                for (int c = 0; c < 8; ++c) {
+                    float p[8];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        float p[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (kFp8) {
-                                const float t = ex2(u2f(x[64 * hf + 8 * c + i]) - mu);
-                                l4[i & 3] += t;
-                                p[i] = t * sig[64 * hf + 8 * c + i];
-                            } else {
-                                p[i] = ex2(fmaf(u2f(x[64 * hf + 8 * c + i]), c2, -mu));
-                                l4[i & 3] += p[i];
-                            }
-                        }
-                        // bf16 (fp16) weights for the MMA; the sum keeps the float32 values, so the
-                        // roundings (half a step, 2^-8 relative) average out in the output
-                        *reinterpret_cast<uint4 *>(pl + sw128_offset(r, c)) =
-                            kFp8 ? make_uint4(pack_f16(p[0], p[1]), pack_f16(p[2], p[3]), pack_f16(p[4], p[5]),
-                                              pack_f16(p[6], p[7]))
-                                 : make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
-                                              pack_bf16(p[6], p[7]));
+                    for (int i = 0; i < 8; ++i) {
+                        p[i] = kFp8 ? ex2(u2f(x[8 * c + i]) - mu) : ex2(fmaf(u2f(x[8 * c + i]), c2, -mu));
+                        l4[i & 3] += p[i];
                     }
+                    if constexpr (kFp8) {
+                        const float4 ga = *reinterpret_cast<const float4 *>(sig + 8 * c);
+                        const float4 gb = *reinterpret_cast<const float4 *>(sig + 8 * c + 4);
+                        p[0] *= ga.x, p[1] *= ga.y, p[2] *= ga.z, p[3] *= ga.w;
+                        p[4] *= gb.x, p[5] *= gb.y, p[6] *= gb.z, p[7] *= gb.w;
+                    }
+                    // bf16 (fp16) weights for the MMA; the sum keeps the float32 values, so the
+                    // roundings (half a step, 2^-8 relative) average out in the output
+                    *reinterpret_cast<uint4 *>(pl + sw128_offset(r, c)) =
+                        kFp8 ? make_uint4(pack_f16(p[0], p[1]), pack_f16(p[2], p[3]), pack_f16(p[4], p[5]),
+                                          pack_f16(p[6], p[7]))
+                             : make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
+                                          pack_bf16(p[6], p[7]));
                 }
                 const float lt = (l4[0] + l4[1]) + (l4[2] + l4[3]);
                 l += kFp8 ? lt * ex2(-te) : lt;
@@ -1055,41 +1057,39 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                 ok = false;
                 break;
             }
-            if (flag) st_remote(r_alpha + (slot * kRows + r) * 4, __float_as_uint(al), r_pfull + slot * 8);
-            if (lane == 0) st_remote(r_flags + (slot * 4 + quad) * 4, flag ? 1u : 0u, r_pfull + slot * 8);
+            if (half == 0) {
+                if (flag) st_remote(r_alpha + (slot * kRows + r) * 4, __float_as_uint(al), r_pfull + slot * 8);
+                if (lane == 0) st_remote(r_flags + (slot * 4 + quad) * 4, flag ? 1u : 0u, r_pfull + slot * 8);
+            }
             __syncwarp();
             if (lane == 0) {
                 // the warp's 32 rows x 64 keys are 4 KB in a row of the staged tile
-                const uint32_t off = slot * kPSlot + quad * 4096;
-                const int parts = !live ? 0 : nk > 64 ? 2 : 1;
-                arrive_expect_remote(r_pfull + slot * 8, parts * 4096 + (flag ? 132 : 4));
-                for (int hf = 0; hf < parts; ++hf)
-                    copy_remote(p_remote + off + hf * 2 * kBlk, smem_u32(p_stage) + off + hf * 2 * kBlk, 4096,
-                                r_pfull + slot * 8);
+                const uint32_t off = slot * kPSlot + half * 2 * kBlk + quad * 4096;
+                arrive_expect_remote(r_pfull + slot * 8, (used ? 4096 : 0) + (half ? 0 : flag ? 132 : 4));
+                if (used) copy_remote(p_remote + off, smem_u32(p_stage) + off, 4096, r_pfull + slot * 8);
             }
         }
         if (!ok) break;
-        // row statistics to the value CTA, the odd tiles' sum joined to the even tiles'
-        // (a piece's result is out before the next piece's first P: see out_done)
-        if (group == 1) {
-            // the piece's last maximum, if the other group's tile had it
-            if (((tile - 1) & 1) == 0 &&
-                !mbar_wait(&sm->m_bar[0][quad], ((tile - 1) >> 1) & 1, a.p.status, &sm->abort))
-                break;
-            const float mf = sm->q.m_run[r];
-            sm->q.l_odd[r] = m != -INFINITY ? l * ex2(m - mf) : 0.f;
+        // row statistics to the value CTA: both halves' sums joined, through the maxima's
+        // place of the next tile's parity (a piece's result is out before the next
+        // piece's first P: see out_done)
+        if (live) {
+            float *lx = reinterpret_cast<float *>(&sm->q.xmax[tile & 1][0][0]);
+            if (half == 1) lx[r] = l;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->l_bar[quad]);
-            if (!mbar_wait(&sm->l_read[quad], piece & 1, a.p.status, &sm->abort)) break;
-        } else {
-            if (!mbar_wait(&sm->l_bar[quad], piece & 1, a.p.status, &sm->abort)) break;
-            const float mf = sm->q.m_run[r], lo = sm->q.l_odd[r];
+            if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
+            if (!mbar_wait(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
+            xphase ^= 1;
+            if (half == 0) l += lx[r];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->l_read[quad]);
-            l = (m != -INFINITY ? l * ex2(m - mf) : 0.f) + lo;
+            if (lane == 0) mbar_arrive(&sm->x_bar[quad]);  // read, before the place is written again
+            if (!mbar_wait(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
+            xphase ^= 1;
+        }
+        if (half == 0) {
             if (piece > 0 && !mbar_wait_cluster(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) break;
             if (live) {
-                st_remote(r_m + r * 4, __float_as_uint(kFp8 ? mf - kShiftFp8 : mf), r_stat);
+                st_remote(r_m + r * 4, __float_as_uint(kFp8 ? m - kShiftFp8 : m), r_stat);
                 st_remote(r_l + r * 4, __float_as_uint(l), r_stat);
             }
             __syncwarp();
@@ -1508,22 +1508,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm->sig_full[i], 1);
-            mbar_init(&sm->sig_free[i], 4);
+            mbar_init(&sm->sig_free[i], 8);
         }
         for (int i = 0; i < kSBufs; ++i) {
             mbar_init(&sm->s_full[i], 1);
-            mbar_init(&sm->s_free[i], 4);
+            mbar_init(&sm->s_free[i], 8);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&sm->m_bar[0][i], 1);
-            mbar_init(&sm->m_bar[1][i], 1);
-            mbar_init(&sm->l_bar[i], 1);
-            mbar_init(&sm->l_read[i], 1);
+            mbar_init(&sm->x_bar[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm->p_free[i], 1);
             mbar_init(&sm->p_got[i], 1);
-            mbar_init(&sm->p_full[i], 4);
+            mbar_init(&sm->p_full[i], 8);
         }
         mbar_init(&sm->out_done, 8);
         mbar_init(&sm->stat_full, 4);
