@@ -229,22 +229,26 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
         : "memory");
     return ok != 0;
 }
-// mbar_wait for a barrier that the other CTA arrives on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint32_t *status,
-                                                  volatile int *abort_flag) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort_flag) return false;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
+// mbar_wait in fewer instructions: the roles' loops wait in some thirty places, and
+// together they have to stay in the instruction cache.  Acquires at cluster scope, for
+// the barriers that the other CTA arrives on.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint32_t *status, volatile int *abort_flag) {
+    uint32_t it = 0;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    while (!mbar_try_wait_cluster(bar, parity)) {
+        if ((++it & 255u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (abort_flag && *abort_flag) return false;
+            if (now - t0 > kWaitLimitNs) {
                 report_status(status, DSA_ERR_TIMEOUT);
-                *abort_flag = 1;
+                if (abort_flag) *abort_flag = 1;
                 return false;
             }
         }
     }
+    return true;
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -515,7 +519,7 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
     uint32_t fills = 0, tile = 0, q_use = 0;  // fills of each stage so far
     bool ok = true;
     auto stage_free = [&](int i) {
-        return fills == 0 || mbar_wait(&sm->k_free[i], (fills - 1) & 1, a.p.status, &sm->abort);
+        return fills == 0 || wait_bar(&sm->k_free[i], (fills - 1) & 1, a.p.status, &sm->abort);
     };
     uint32_t piece = 0, part = 0;  // part: stages filled of the current round
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
@@ -545,10 +549,10 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
             part = 0;
         }
         auto load_query = [&]() {
-            if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) return false;
+            if (piece > 0 && !wait_bar(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) return false;
             if (small)  // the staged P of the last two tiles has left
                 for (uint32_t t = tile > 2 ? tile - 2 : 0; t < tile; ++t)
-                    if (!mbar_wait_cluster(&sm->p_got[t & 1], (t >> 1) & 1, a.p.status, &sm->abort)) return false;
+                    if (!wait_bar(&sm->p_got[t & 1], (t >> 1) & 1, a.p.status, &sm->abort)) return false;
             ++q_use;
             if (lane == 0) mbar_arrive_expect_tx(&sm->q_full, (small ? kNB : 2) * kBlk);
             __syncwarp();
@@ -572,7 +576,7 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
                 if (lane == 0) report_status(a.p.status, DSA_ERR_INVALID);
             }
             // key_ok of this tile's S buffer: its previous tile has been read
-            if (tile >= kSBufs && !mbar_wait(&sm->s_free[tile % kSBufs], (tile / kSBufs - 1) & 1, a.p.status, &sm->abort)) {
+            if (tile >= kSBufs && !wait_bar(&sm->s_free[tile % kSBufs], (tile / kSBufs - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
@@ -604,22 +608,23 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
     __syncwarp();
     for (uint32_t i = 0; i < kKStages; ++i) {
         const uint32_t n = fills + (i < part ? 1 : 0);
-        if (n > 0) mbar_wait(&sm->k_full[i], (n - 1) & 1, a.p.status, nullptr);
+        if (n > 0) wait_bar(&sm->k_full[i], (n - 1) & 1, a.p.status, nullptr);
     }
-    if (q_use > 0) mbar_wait(&sm->q_full, (q_use - 1) & 1, a.p.status, nullptr);
+    if (q_use > 0) wait_bar(&sm->q_full, (q_use - 1) & 1, a.p.status, nullptr);
 }
 
-// One unit's 36 MMAs into S buffer kBuf.  Tensor memory is allocated whole, so its
+// One unit's 36 MMAs into S buffer buf.  Tensor memory is allocated whole, so its
 // base is 0 and every address and descriptor here is a constant: an operand that
 // has to be moved to a uniform register first costs the issuing thread more than
 // the 64 cycles an MMA takes (measured: 115 cycles per MMA with a computed stage).
 // A tile of 64 keys or fewer multiplies what an earlier tile left in the upper
 // half too; those columns are not read.
-template <int kBuf>
-__device__ __forceinline__ bool score_tile(const TcArgs &a, Small *sm, uint32_t q_addr, uint32_t k_addr, uint32_t parity) {
+__device__ __forceinline__ bool score_tile(const TcArgs &a, Small *sm, uint32_t q_addr, uint32_t k_addr, uint32_t parity,
+                                           uint32_t buf) {
+    const uint32_t d = kKeys * buf;
 #pragma unroll
     for (int i = 0; i < kKStages; ++i) {
-        if (!mbar_wait(&sm->k_full[i], parity, a.p.status, &sm->abort)) return false;
+        if (!wait_bar(&sm->k_full[i], parity, a.p.status, &sm->abort)) return false;
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < kKBlocks; ++j) {
@@ -628,16 +633,16 @@ __device__ __forceinline__ bool score_tile(const TcArgs &a, Small *sm, uint32_t 
             if (kb < kQTmem) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    umma_bf16_ta(kKeys * kBuf, kQCol + 32 * kb + 8 * k, bd + 2 * k, kIdescS, kb + k > 0 ? 1u : 0u);
+                    umma_bf16_ta(d, kQCol + 32 * kb + 8 * k, bd + 2 * k, kIdescS, kb + k > 0 ? 1u : 0u);
             } else {
                 const uint64_t ad = sdesc_sw128(q_addr, 16, 1024);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_bf16(kKeys * kBuf, ad + 2 * k, bd + 2 * k, kIdescS, 1u);
+                for (int k = 0; k < 4; ++k) umma_bf16(d, ad + 2 * k, bd + 2 * k, kIdescS, 1u);
             }
         }
         umma_commit(&sm->k_free[i]);
     }
-    umma_commit(&sm->s_full[kBuf]);
+    umma_commit(&sm->s_full[buf]);
     return true;
 }
 
@@ -647,11 +652,11 @@ __device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *p_
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
         // query blocks to tensor memory, after the previous piece's products
-        if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
+        if (piece > 0 && !wait_bar(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
         if (w.rows() > 64) {
 #pragma unroll
             for (int i = 0; i < kKStages; ++i) {
-                if (!ok || !mbar_wait(&sm->k_full[i], fills & 1, a.p.status, &sm->abort)) {
+                if (!ok || !wait_bar(&sm->k_full[i], fills & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     continue;
                 }
@@ -669,7 +674,7 @@ __device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *p_
             ++fills;
             if (!ok) break;
         }
-        if (!mbar_wait(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
+        if (!wait_bar(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
         if (w.rows() <= 64) {
             // (rows 64..127 take what follows in shared memory: rows of no token)
             tc_fence_after();
@@ -681,17 +686,17 @@ __device__ void score_mma(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t *p_
         }
         for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile, ++fills) {
             const uint32_t buf = tile % kSBufs;
-            if (tile >= kSBufs && !mbar_wait(&sm->s_free[buf], (tile / kSBufs - 1) & 1, a.p.status, &sm->abort)) {
+            if (tile >= kSBufs && !wait_bar(&sm->s_free[buf], (tile / kSBufs - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            ok = buf ? score_tile<1>(a, sm, q_addr, k_addr, fills & 1) : score_tile<0>(a, sm, q_addr, k_addr, fills & 1);
+            ok = score_tile(a, sm, q_addr, k_addr, fills & 1, buf);
         }
         if (ok) umma_commit(&sm->q_free);
     }
     umma_commit(&sm->fin);
-    mbar_wait(&sm->fin, 0, a.p.status, nullptr);
+    wait_bar(&sm->fin, 0, a.p.status, nullptr);
 }
 
 // Packed FP8 rows, score CTA.  q = s (q1 + q2) with q1, q2 in E4M3 and s a power of
@@ -710,7 +715,7 @@ __device__ void score_producer_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, ui
     uint32_t tile = 0, piece = 0, q_use = 0;
     bool ok = true;
     auto stage_free = [&](int i) {
-        return fills[i] == 0 || mbar_wait(&sm->k_free[i], (fills[i] - 1) & 1, a.p.status, &sm->abort);
+        return fills[i] == 0 || wait_bar(&sm->k_free[i], (fills[i] - 1) & 1, a.p.status, &sm->abort);
     };
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
         Box x = {a.p.n_pages, 0, false};
@@ -736,10 +741,10 @@ __device__ void score_producer_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, ui
             if (!ok) break;
         }
         auto load_query = [&]() {
-            if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) return false;
+            if (piece > 0 && !wait_bar(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) return false;
             if (small)  // the staged P of the last two tiles has left
                 for (uint32_t t = tile > 2 ? tile - 2 : 0; t < tile; ++t)
-                    if (!mbar_wait_cluster(&sm->p_got[t & 1], (t >> 1) & 1, a.p.status, &sm->abort)) return false;
+                    if (!wait_bar(&sm->p_got[t & 1], (t >> 1) & 1, a.p.status, &sm->abort)) return false;
             ++q_use;
             if (lane == 0) mbar_arrive_expect_tx(&sm->q_full, (small ? 9 : 2) * kBlk);
             __syncwarp();
@@ -782,8 +787,8 @@ __device__ void score_producer_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, ui
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 3; ++i)
-        if (fills[i] > 0) mbar_wait(&sm->k_full[i], (fills[i] - 1) & 1, a.p.status, nullptr);
-    if (q_use > 0) mbar_wait(&sm->q_full, (q_use - 1) & 1, a.p.status, nullptr);
+        if (fills[i] > 0) wait_bar(&sm->k_full[i], (fills[i] - 1) & 1, a.p.status, nullptr);
+    if (q_use > 0) wait_bar(&sm->q_full, (q_use - 1) & 1, a.p.status, nullptr);
 }
 
 // Row scales of every key tile to shared memory, divided by the tile's largest power
@@ -810,7 +815,7 @@ __device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
             int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
             e = mx > 0.f ? min(max(e, -120), 120) : 0;
             const float down = u2f(static_cast<uint32_t>(127 - e) << 23);
-            if (tile >= 2 && !mbar_wait(&sm->sig_free[tile & 1], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) return;
+            if (tile >= 2 && !wait_bar(&sm->sig_free[tile & 1], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) return;
             *reinterpret_cast<float4 *>(&sm->q.sigma[tile & 1][4 * lane]) =
                 make_float4(v[0] * down, v[1] * down, v[2] * down, v[3] * down);
             if (lane == 0) {
@@ -825,7 +830,7 @@ __device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
 template <int kSt>
 __device__ __forceinline__ bool score_tile_fp8(const TcArgs &a, Small *sm, uint32_t q_addr, uint32_t c_addr, uint32_t r_addr,
                                                uint32_t parity, uint32_t parity_rope) {
-    if (!mbar_wait(&sm->k_full[kSt], parity, a.p.status, &sm->abort)) return false;
+    if (!wait_bar(&sm->k_full[kSt], parity, a.p.status, &sm->abort)) return false;
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < kLatent / 32; ++k) {
@@ -834,7 +839,7 @@ __device__ __forceinline__ bool score_tile_fp8(const TcArgs &a, Small *sm, uint3
         umma_e4m3_ta(0, kQCol + 128 + 8 * k, bd, kIdescS8, 1u);
     }
     umma_commit(&sm->k_free[kSt]);
-    if (!mbar_wait(&sm->k_full[2], parity_rope, a.p.status, &sm->abort)) return false;
+    if (!wait_bar(&sm->k_full[2], parity_rope, a.p.status, &sm->abort)) return false;
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -849,11 +854,11 @@ __device__ void score_mma_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t
     uint32_t tile = 0, piece = 0, fill0 = 0, fill1 = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
-        if (piece > 0 && !mbar_wait(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
+        if (piece > 0 && !wait_bar(&sm->q_free, (piece - 1) & 1, a.p.status, &sm->abort)) break;
         if (w.rows() > 64) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (!ok || !mbar_wait(&sm->k_full[i], (i ? fill1 : fill0) & 1, a.p.status, &sm->abort)) {
+                if (!ok || !wait_bar(&sm->k_full[i], (i ? fill1 : fill0) & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     continue;
                 }
@@ -868,7 +873,7 @@ __device__ void score_mma_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t
             ++fill1;
             if (!ok) break;
         }
-        if (!mbar_wait(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
+        if (!wait_bar(&sm->q_full, piece & 1, a.p.status, &sm->abort)) break;
         if (w.rows() <= 64) {
             tc_fence_after();
 #pragma unroll
@@ -876,7 +881,7 @@ __device__ void score_mma_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t
                 tmem_copy(kQCol + 8 * k, sdesc_sw128(p_addr + (k >> 2) * kBlk, 16, 1024) + 2 * (k & 3));
         }
         for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
-            if (tile >= 1 && !mbar_wait(&sm->s_free[0], (tile - 1) & 1, a.p.status, &sm->abort)) {
+            if (tile >= 1 && !wait_bar(&sm->s_free[0], (tile - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
@@ -889,7 +894,7 @@ __device__ void score_mma_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t
         if (ok) umma_commit(&sm->q_free);
     }
     umma_commit(&sm->fin);
-    mbar_wait(&sm->fin, 0, a.p.status, nullptr);
+    wait_bar(&sm->fin, 0, a.p.status, nullptr);
 }
 
 // Softmax.  Warp w: rows 32 (w & 3) + lane, keys 64 (w >> 2) .. + 63 of every tile;
@@ -928,8 +933,8 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         for (int kt = w.k0; kt < w.k1; ++kt, ++tile) {
             const uint32_t slot = tile & 1;  // of P, and of bf16's S buffers
             const uint32_t sbuf = kFp8 ? 0 : slot;
-            if ((kFp8 && !mbar_wait(&sm->sig_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) ||
-                !mbar_wait(&sm->s_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
+            if ((kFp8 && !wait_bar(&sm->sig_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) ||
+                !wait_bar(&sm->s_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
@@ -994,7 +999,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                 sm->q.xmax[slot][half][r] = static_cast<uint16_t>(__float_as_uint(mx) >> 16);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
-                if (!mbar_wait(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) {
+                if (!wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
@@ -1010,7 +1015,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             }
             const bool flag = __any_sync(0xffffffffu, al != 1.f);
             // the staged tile two back has left
-            if (tile >= 2 && !mbar_wait_cluster(&sm->p_got[slot], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) {
+            if (tile >= 2 && !wait_bar(&sm->p_got[slot], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
@@ -1049,11 +1054,11 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                 if (lane == 0) mbar_arrive(&sm->sig_free[slot]);
             }
             // (the value CTA stages a piece's result in the P slots)
-            if (kt < w.k0 + 2 && piece > 0 && !mbar_wait_cluster(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) {
+            if (kt < w.k0 + 2 && piece > 0 && !wait_bar(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
-            if (tile >= 2 && !mbar_wait_cluster(&sm->p_free[slot], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) {
+            if (tile >= 2 && !wait_bar(&sm->p_free[slot], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
@@ -1078,16 +1083,16 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             if (half == 1) lx[r] = l;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
-            if (!mbar_wait(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
+            if (!wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
             xphase ^= 1;
             if (half == 0) l += lx[r];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->x_bar[quad]);  // read, before the place is written again
-            if (!mbar_wait(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
+            if (!wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
             xphase ^= 1;
         }
         if (half == 0) {
-            if (piece > 0 && !mbar_wait_cluster(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) break;
+            if (piece > 0 && !wait_bar(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) break;
             if (live) {
                 st_remote(r_m + r * 4, __float_as_uint(kFp8 ? m - kShiftFp8 : m), r_stat);
                 st_remote(r_l + r * 4, __float_as_uint(l), r_stat);
@@ -1112,7 +1117,7 @@ __device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const 
             const int khs = w.keys(kt) > 64 ? 2 : 1;
             for (int g = 0; g < 2 * khs; ++g, ++it) {
                 const int d = g / khs, kh = g % khs, st = it % kVStages;  // dims 256 d .., keys 64 kh ..
-                if (it >= kVStages && !mbar_wait(&sm->v_free[st], (it / kVStages - 1) & 1, a.p.status, &sm->abort)) {
+                if (it >= kVStages && !wait_bar(&sm->v_free[st], (it / kVStages - 1) & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
@@ -1127,7 +1132,7 @@ __device__ void value_producer(const TcArgs &a, Small *sm, uint8_t *v_sm, const 
     }
     __syncwarp();
     for (uint32_t i = it > kVStages ? it - kVStages : 0; i < it; ++i)
-        mbar_wait(&sm->v_full[i % kVStages], (i / kVStages) & 1, a.p.status, nullptr);
+        wait_bar(&sm->v_full[i % kVStages], (i / kVStages) & 1, a.p.status, nullptr);
 }
 
 // Packed FP8 rows: units of 32 keys x 512 codes.
@@ -1143,7 +1148,7 @@ __device__ void value_producer_fp8(const TcArgs &a, Small *sm, uint8_t *raw_sm, 
             const int units = (w.keys(kt) + 31) / 32;
             for (int u = 0; u < units; ++u, ++it) {
                 const int st = it % kRawStages;
-                if (it >= kRawStages && !mbar_wait(&sm->v_free[st], (it / kRawStages - 1) & 1, a.p.status, &sm->abort)) {
+                if (it >= kRawStages && !wait_bar(&sm->v_free[st], (it / kRawStages - 1) & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
@@ -1157,7 +1162,7 @@ __device__ void value_producer_fp8(const TcArgs &a, Small *sm, uint8_t *raw_sm, 
     }
     __syncwarp();
     for (uint32_t i = it > kRawStages ? it - kRawStages : 0; i < it; ++i)
-        mbar_wait(&sm->v_full[i % kRawStages], (i / kRawStages) & 1, a.p.status, nullptr);
+        wait_bar(&sm->v_full[i % kRawStages], (i / kRawStages) & 1, a.p.status, nullptr);
 }
 
 // One unit's codes to fp16 (exact), this warp's quarter (of four): raw [4 groups of 8 keys][4 x
@@ -1188,7 +1193,7 @@ __device__ __forceinline__ bool post_command(const TcArgs &a, Small *sm, int cmd
     umma_commit(&sm->cmd_full);
     const uint32_t ph = phase;
     phase ^= 1;
-    return !wait || mbar_wait(&sm->cmd_done, ph, a.p.status, &sm->abort);
+    return !wait || wait_bar(&sm->cmd_done, ph, a.p.status, &sm->abort);
 }
 
 template <bool kFp8>
@@ -1203,7 +1208,7 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
         for (int kt = w.k0; ok && kt < w.k1; ++kt, ++tile) {
             const uint32_t slot = tile & 1;
             const int khs = w.keys(kt) > 64 ? 2 : 1;
-            if (!mbar_wait_cluster(&sm->p_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
+            if (!wait_bar(&sm->p_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
@@ -1225,7 +1230,7 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
                 const int units = (w.keys(kt) + 31) / 32;
                 for (int u = 0; u < units; ++u, ++it) {
                     const int st = it % kHStages;
-                    if (!mbar_wait(&sm->h_full[st], (it / kHStages) & 1, a.p.status, &sm->abort)) {
+                    if (!wait_bar(&sm->h_full[st], (it / kHStages) & 1, a.p.status, &sm->abort)) {
                         ok = false;
                         break;
                     }
@@ -1247,7 +1252,7 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
             }
             for (int g = 0; !kFp8 && g < 2 * khs; ++g, ++it) {
                 const int d = g / khs, kh = g % khs, st = it % kVStages;
-                if (!mbar_wait(&sm->v_full[st], (it / kVStages) & 1, a.p.status, &sm->abort)) {
+                if (!wait_bar(&sm->v_full[st], (it / kVStages) & 1, a.p.status, &sm->abort)) {
                     ok = false;
                     break;
                 }
@@ -1287,7 +1292,7 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
     if (lane == 0) {
         post_command(a, sm, kCmdExit, cphase, false);
         umma_commit(&sm->fin);
-        mbar_wait(&sm->fin, 0, a.p.status, nullptr);
+        wait_bar(&sm->fin, 0, a.p.status, nullptr);
     }
     __syncwarp();
 }
@@ -1373,7 +1378,7 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
                 continue;
             }
             idle = 0;
-        } else if (!mbar_wait(&sm->cmd_full, cphase, a.p.status, &sm->abort)) {
+        } else if (!wait_bar(&sm->cmd_full, cphase, a.p.status, &sm->abort)) {
             break;
         }
         cphase ^= 1;
@@ -1396,7 +1401,7 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
                 tmem_st_wait();
             }
         } else {
-            if (!mbar_wait_cluster(&sm->stat_full, piece & 1, a.p.status, &sm->abort)) break;
+            if (!wait_bar(&sm->stat_full, piece & 1, a.p.status, &sm->abort)) break;
             const int rows = w.rows();
             const bool live = r < rows;
             const float l = sm->v.l[r], m = sm->v.m[r];
