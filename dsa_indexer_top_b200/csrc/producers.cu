@@ -125,6 +125,9 @@ __global__ void __launch_bounds__(kEpiThreads) cache_write_epilogue_kernel(const
         sv += d * d;
     }
     const float rstd = 1.f / sqrtf(block_sum(sv, red) / kIdxDim + a.eps);
+    // both RoPE parts turn by the same angles (in double: most of this kernel's latency)
+    float rc = 0.f, rs = 0.f;
+    if (threadIdx.x < kRope / 2) rope_cs(pos, threadIdx.x, a.log2_theta, rc, rs);
     if (a.kv) {
         __nv_bfloat16 *row = static_cast<__nv_bfloat16 *>(a.kv) + static_cast<int64_t>(seq) * a.kv_seq_stride +
                              static_cast<int64_t>(row_at) * a.kv_row_stride;
@@ -132,8 +135,7 @@ __global__ void __launch_bounds__(kEpiThreads) cache_write_epilogue_kernel(const
             row[f] = __float2bfloat16_rn(y[f] * rms * a.rms_weight[f]);
         if (threadIdx.x < kRope / 2) {
             const int i = threadIdx.x;
-            float c, s;
-            rope_cs(pos, i, a.log2_theta, c, s);
+            const float c = rc, s = rs;
             const float x0 = y[kLatent + 2 * i], x1 = y[kLatent + 2 * i + 1];
             row[kLatent + 2 * i] = __float2bfloat16_rn(x0 * c - x1 * s);
             row[kLatent + 2 * i + 1] = __float2bfloat16_rn(x0 * s + x1 * c);
@@ -148,8 +150,7 @@ __global__ void __launch_bounds__(kEpiThreads) cache_write_epilogue_kernel(const
             key[f] = __float2bfloat16_rn((yk[f] - mu) * rstd * a.ln_weight[f] + a.ln_bias[f]);
         if (threadIdx.x < kRope / 2) {
             const int i = threadIdx.x, f0 = kIdxDim - kRope + 2 * i;
-            float c, s;
-            rope_cs(pos, i, a.log2_theta, c, s);
+            const float c = rc, s = rs;
             const float x0 = (yk[f0] - mu) * rstd * a.ln_weight[f0] + a.ln_bias[f0];
             const float x1 = (yk[f0 + 1] - mu) * rstd * a.ln_weight[f0 + 1] + a.ln_bias[f0 + 1];
             key[f0] = __float2bfloat16_rn(x0 * c - x1 * s);
@@ -201,10 +202,10 @@ size_t al256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Split-K plan of the cache-row GEMM (M = tokens, N = 704, K = hidden): about
 // one CTA per SM on a 148-SM part, at least 4 blocks of 64 along K per split.
-void cache_plan(int n_tok, int hidden, int &m_tiles, int &k_splits, int &kb_per_split) {
+void cache_plan(int n_tok, int hidden, int bn, int &m_tiles, int &k_splits, int &kb_per_split) {
     const int kb = (hidden + 63) / 64;
     m_tiles = n_tok > 0 ? (n_tok + 127) / 128 : 1;
-    const int tiles = m_tiles * ((kProjFeatures + 127) / 128);
+    const int tiles = m_tiles * ((kProjFeatures + bn - 1) / bn);
     int s = 144 / tiles;
     s = s < 1 ? 1 : s;
     const int max_s = kb / 4 > 0 ? kb / 4 : 1;
@@ -213,9 +214,20 @@ void cache_plan(int n_tok, int hidden, int &m_tiles, int &k_splits, int &kb_per_
     k_splits = (kb + kb_per_split - 1) / kb_per_split;
 }
 
+// The paged writer's contraction.  Tiles of 256 output columns from 1024 tokens on
+// (the operands' way from L2 bounds the GEMM, and wider tiles read the hidden states
+// half as often: 2048 tokens 31.7 us against 46.6, 1024 23.2 against 24.2, but 512
+// 20.5 against 17.3); CUDA cores up to 4 tokens (11.5 us; 13 tokens 26.2 us against
+// 10.6 on the tensor cores).  The contiguous writer keeps its plan, and with it the
+// order of its sums.
+int paged_bn(int n_tok) { return n_tok >= 1024 ? 256 : 128; }
+constexpr int kPagedSkinnyMax = 4;
+
 size_t cache_ws_bytes(int n_tok, int hidden) {
-    int mt, ks, kbs;
-    cache_plan(n_tok, hidden, mt, ks, kbs);
+    int mt, ks, kbs, ks_paged;
+    cache_plan(n_tok, hidden, 128, mt, ks, kbs);
+    cache_plan(n_tok, hidden, paged_bn(n_tok), mt, ks_paged, kbs);
+    ks = ks > ks_paged ? ks : ks_paged;
     return kStatus + al256(static_cast<size_t>(ks) * n_tok * kProjFeatures * sizeof(float));
 }
 
@@ -264,14 +276,15 @@ static dsa_status write_rows(const dsa_cache_writer *cw, const int32_t *slot_map
     g.N = kProjFeatures;
     g.K = cw->hidden;
     g.batch = 1;
-    cache_plan(cw->n_tok, cw->hidden, g.m_tiles, g.k_splits, g.kb_per_split);
+    const int bn = slot_map ? paged_bn(cw->n_tok) : 128;
+    cache_plan(cw->n_tok, cw->hidden, bn, g.m_tiles, g.k_splits, g.kb_per_split);
     float *y = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kStatus);
     g.out_f32 = y;
     g.ldc = kProjFeatures;
     g.s_batch = 0;
     g.s_split = static_cast<int64_t>(cw->n_tok) * kProjFeatures;
     g.status = static_cast<uint32_t *>(ws);
-    if (cw->n_tok <= kSkinnyMaxM) {
+    if (cw->n_tok <= (slot_map ? kPagedSkinnyMax : kSkinnyMaxM)) {
         // decode-sized batch: stream the weights once on CUDA cores (same partials)
         GemmSkinnyArgs k = {};
         k.M = cw->n_tok;
@@ -298,9 +311,9 @@ static dsa_status write_rows(const dsa_cache_writer *cw, const int32_t *slot_map
         CUtensorMap ta, tb;
         if (!encode_gemm_operand(&ta, cw->h, cw->hidden, cw->n_tok, 1, cw->h_row_stride, 0, 128, &g.a_batch_inner))
             return DSA_ERR_INVALID;
-        if (!encode_gemm_operand(&tb, cw->w, cw->hidden, kProjFeatures, 1, cw->hidden, 0, 128, &g.b_batch_inner))
+        if (!encode_gemm_operand(&tb, cw->w, cw->hidden, kProjFeatures, 1, cw->hidden, 0, bn, &g.b_batch_inner))
             return DSA_ERR_INVALID;
-        if (launch_gemm_tc(128, ta, tb, g, st) != cudaSuccess) return DSA_ERR_CUDA;
+        if (launch_gemm_tc(bn, ta, tb, g, st) != cudaSuccess) return DSA_ERR_CUDA;
     }
     CacheWriteArgs e;
     e.y = y;
