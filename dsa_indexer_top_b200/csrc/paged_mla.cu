@@ -150,8 +150,8 @@ struct TcArgs {
     int tok_tile;       // tokens per row tile
     int box;            // rows per TMA copy (divides page_rows, 8..64)
     Meta *meta;         // [clusters]
-    float *part_ml;     // [2 * clusters][128][2] maximum (log2), sum
-    float *part_o;      // [2 * clusters][128][512]
+    float *part_ml;     // [2 * clusters][2][128] maximum (log2), sum
+    float *part_o;      // [2 * clusters][512][128]
     const uint8_t *q8;  // packed FP8 rows: the queries' latent part as two E4M3 terms [rows][2][512]
     const float *q8_scale;  // [rows] their power-of-two scale
 };
@@ -1409,60 +1409,49 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
             const bool whole = w.k0 == 0 && w.k1 == w.nk;
             const int64_t row = w.row0() + r;
             const int64_t pslot = 2 * cluster + (w.k0 == 0 ? 1 : 0);
-            if (32 * quad < rows) {
-                // 64 columns at a time through the warp's 8 KB of the P slots (16-byte pieces
+            if (32 * quad < rows && whole) {
+                // 128 columns at a time through the warp's 8 KB of the P slots (16-byte pieces
                 // exchanged by row, so that neither side conflicts), then whole rows to memory:
-                // a lane's own 16-byte stores, 2 KB apart, took four times as long
+                // a lane's own 16-byte stores, 1 KB apart, took four times as long
                 uint8_t *st = stage + warp * 8192;
                 const int n_live = min(32, rows - 32 * quad);
-                const int64_t row_w = row - lane;  // the warp's first row
-                if (whole) {
+                uint8_t *o = static_cast<uint8_t *>(a.p.out) + ((row - lane) * kLatent + 256 * half) * 2;
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 128) {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            uint32_t x[32];
-                            tmem_ld32(tb + c + 32 * g, x);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                *reinterpret_cast<uint4 *>(st + lane * 256 + (((4 * g + i / 8) ^ (lane & 15)) << 4)) =
-                                    make_uint4(pack_bf16(u2f(x[i]) * inv, u2f(x[i + 1]) * inv),
-                                               pack_bf16(u2f(x[i + 2]) * inv, u2f(x[i + 3]) * inv),
-                                               pack_bf16(u2f(x[i + 4]) * inv, u2f(x[i + 5]) * inv),
-                                               pack_bf16(u2f(x[i + 6]) * inv, u2f(x[i + 7]) * inv));
-                        }
-                        if (c == 128) fence_proxy_async_smem();  // (the slots are next written by a copy)
-                        __syncwarp();
-                        uint8_t *o = static_cast<uint8_t *>(a.p.out) + (row_w * kLatent + 256 * half + c) * 2;
-                        put_rows(o, kLatent * 2, st, lane, n_live);
-                        __syncwarp();
-                    }
-                } else {
+                for (int c = 0; c < 256; c += 128) {
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 64) {
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t x[32];
+                        tmem_ld32(tb + c + 32 * g, x);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            uint32_t x[32];
-                            tmem_ld32(tb + c + 32 * g, x);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<uint4 *>(st + lane * 256 + (((8 * g + i / 4) ^ (lane & 15)) << 4)) =
-                                    make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                        }
-                        if (c == 192) fence_proxy_async_smem();
-                        __syncwarp();
-                        put_rows(reinterpret_cast<uint8_t *>(a.part_o + (pslot * kRows + 32 * quad) * kLatent + 256 * half + c),
-                                 kLatent * 4, st, lane, n_live);
-                        __syncwarp();
+                        for (int i = 0; i < 32; i += 8)
+                            *reinterpret_cast<uint4 *>(st + lane * 256 + (((4 * g + i / 8) ^ (lane & 15)) << 4)) =
+                                make_uint4(pack_bf16(u2f(x[i]) * inv, u2f(x[i + 1]) * inv),
+                                           pack_bf16(u2f(x[i + 2]) * inv, u2f(x[i + 3]) * inv),
+                                           pack_bf16(u2f(x[i + 4]) * inv, u2f(x[i + 5]) * inv),
+                                           pack_bf16(u2f(x[i + 6]) * inv, u2f(x[i + 7]) * inv));
                     }
+                    if (c == 128) fence_proxy_async_smem();  // (the slots are next written by a copy)
+                    __syncwarp();
+                    put_rows(o + 2 * c, kLatent * 2, st, lane, n_live);
+                    __syncwarp();
+                }
+            } else if (32 * quad < rows) {
+                // partials [column][row]: a warp's 32 rows are one line, as they come
+                float *po = a.part_o + (pslot * kLatent + 256 * half) * kRows + r;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(tb + c, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) po[(c + i) * kRows] = u2f(x[i]);
                 }
             }
             if (live && half == 0) {
                 if (!whole) {
-                    a.part_ml[(pslot * kRows + r) * 2] = m;
-                    a.part_ml[(pslot * kRows + r) * 2 + 1] = l;
+                    a.part_ml[pslot * 2 * kRows + r] = m;
+                    a.part_ml[(pslot * 2 + 1) * kRows + r] = l;
                 } else if (a.p.lse) {
                     a.p.lse[row] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
                 }
@@ -1652,65 +1641,70 @@ __global__ void __launch_bounds__(256) split_queries_kernel(const __nv_bfloat16 
 
 // Merge of the row tiles that a cut divided: o = sum_i 2^(m_i - M) o_i / sum_i
 // 2^(m_i - M) l_i over the parts, the first in its cluster's second slot, the
-// others in the next clusters' first slots.  One CTA per (cluster, 4 rows); most
-// find nothing to do.  Bound by latency: two round trips to L2.
-constexpr int kMergeRows = 4;   // 128 threads each
-constexpr int kMaxParts = 256;  // clusters of any GPU this runs on
+// others in the next clusters' first slots.  One CTA per (cluster, 32 rows, 64
+// columns); most find nothing to do.  Bound by latency: two round trips to L2.
+constexpr int kMergeCols = 64;  // columns and rows of a CTA
+constexpr int kMergeRows = 32;
+constexpr int kMaxParts = 96;  // clusters at most (74 on 148 SMs)
 
-__global__ void __launch_bounds__(128 * kMergeRows) paged_mla_merge_kernel(const TcArgs a) {
-    __shared__ float wt[kMergeRows][kMaxParts];
+__global__ void __launch_bounds__(256) paged_mla_merge_kernel(const TcArgs a) {
+    __shared__ float wt[kMaxParts][kMergeRows];
+    __shared__ float tr[kMergeCols][kMergeRows + 1];
     griddep_wait();
-    const int c = blockIdx.x;
+    const int c = blockIdx.x, r0 = blockIdx.y * kMergeRows, c0 = blockIdx.z * kMergeCols;
     const Meta me = a.meta[c];
-    const int g = threadIdx.x >> 7, r = blockIdx.y * kMergeRows + g;
-    if (blockIdx.y * kMergeRows >= me.rows || me.parts == 0) return;
-    const int d = (threadIdx.x & 127) * 4, lane = threadIdx.x & 31;
-    const int64_t slot0 = static_cast<int64_t>(2 * c + 1) * kRows + r;                        // the first part
-    auto slot = [&](int i) { return i == 0 ? slot0 : static_cast<int64_t>(2 * (c + i)) * kRows + r; };
-    // the first eight parts' values are on their way while the weights are found
-    float4 x[8];
+    if (r0 >= me.rows || me.parts == 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = r0 + lane;
+    auto slot = [&](int i) { return static_cast<int64_t>(2 * (c + i) + (i == 0 ? 1 : 0)); };  // the first part is a head
+    // a row per lane, eight columns per warp; the first two parts' values are on their
+    // way while the weights are found
+    const float *po = a.part_o + static_cast<int64_t>(c0 + 8 * warp) * kRows + r;
+    auto fetch = [&](float (&x)[8], int i) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        x[i] = i < me.parts ? *reinterpret_cast<const float4 *>(a.part_o + slot(i) * kLatent + d)
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
-    if ((threadIdx.x & 127) < 32) {
-        float M = -INFINITY, L = 0.f;
-        for (int i = lane; i < me.parts; i += 32) M = fmaxf(M, a.part_ml[slot(i) * 2]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (int i = lane; i < me.parts; i += 32) {
-            const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(i) * 2);
-            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-            wt[g][i] = w;
-            L += w * ml.y;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        for (int i = lane; i < me.parts; i += 32) wt[g][i] *= inv;
-        if (lane == 0 && r < me.rows && a.p.lse)
-            a.p.lse[static_cast<int64_t>(me.row0) + r] = L > 0.f ? M * kLn2 + logf(L) : -INFINITY;
-    }
-    __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4 &v, float w) {
-        // (a part without weight may have left anything, and 0 x NaN is NaN)
-        if (w != 0.f) acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+        for (int k = 0; k < 8; ++k) x[k] = i < me.parts ? po[(slot(i) * kLatent + k) * kRows] : 0.f;
     };
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < me.parts) add(x[i], wt[g][i]);
-    for (int i0 = 8; i0 < me.parts; i0 += 8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i0 + i < me.parts) x[i] = *reinterpret_cast<const float4 *>(a.part_o + slot(i0 + i) * kLatent + d);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i0 + i < me.parts) add(x[i], wt[g][i0 + i]);
+    float x[2][8];
+    fetch(x[0], 0);
+    fetch(x[1], 1);
+    // weights: warp w takes parts w, w + 8, ..
+    float M = -INFINITY;
+    for (int i = 0; i < me.parts; ++i) M = fmaxf(M, a.part_ml[(slot(i) * 2) * kRows + r]);
+    float L = 0.f;
+    for (int i = 0; i < me.parts; ++i) {
+        const float m = a.part_ml[(slot(i) * 2) * kRows + r], l = a.part_ml[(slot(i) * 2 + 1) * kRows + r];
+        const float w = m == -INFINITY ? 0.f : exp2f(m - M);
+        if ((i & 7) == warp) wt[i][lane] = w;
+        L += w * l;
     }
-    if (r < me.rows)
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.p.out) + (static_cast<int64_t>(me.row0) + r) * kLatent + d) =
-            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    if (warp == 0 && blockIdx.z == 0 && r < me.rows && a.p.lse)
+        a.p.lse[static_cast<int64_t>(me.row0) + r] = L > 0.f ? M * kLn2 + logf(L) : -INFINITY;
+    __syncthreads();
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int i = 0; i < me.parts; i += 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // (a part without weight may have left anything, and 0 x NaN is NaN)
+            const float w = i + h < me.parts ? wt[i + h][lane] : 0.f;
+            if (w != 0.f)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] += w * x[h][k];
+            fetch(x[h], i + h + 2);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) tr[8 * warp + k][lane] = acc[k] * inv;
+    __syncthreads();
+    // 64 columns of a row are 128 bytes of the output
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int row = r0 + 4 * warp + k;
+        if (row < me.rows)
+            reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.p.out) +
+                                         (static_cast<int64_t>(me.row0) + row) * kLatent + c0)[lane] =
+                pack_bf16(tr[2 * lane][4 * warp + k], tr[2 * lane + 1][4 * warp + k]);
+    }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1805,7 +1799,7 @@ cudaError_t launch_paged_mla_tc(const PagedMlaArgs &p, void *scratch, int num_sm
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(2 * a.clusters), dim3(kThreads), smem, st, a, m);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_mla_merge_kernel, dim3(a.clusters, kRows / kMergeRows), dim3(128 * kMergeRows), 0, st, a);
+    return launch_pdl(paged_mla_merge_kernel, dim3(a.clusters, kRows / kMergeRows, kLatent / kMergeCols), dim3(256), 0, st, a);
 }
 
 }  // namespace dsa
