@@ -827,25 +827,27 @@ __device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
         }
 }
 
-template <int kSt>
 __device__ __forceinline__ bool score_tile_fp8(const TcArgs &a, Small *sm, uint32_t q_addr, uint32_t c_addr, uint32_t r_addr,
-                                               uint32_t parity, uint32_t parity_rope) {
-    if (!wait_bar(&sm->k_full[kSt], parity, a.p.status, &sm->abort)) return false;
+                                               int st, uint32_t parity, uint32_t parity_rope) {
+    if (!wait_bar(&sm->k_full[st], parity, a.p.status, &sm->abort)) return false;
     tc_fence_after();
+    uint64_t bd = sdesc_sw128(c_addr + st * kCodes, 16, 4096);
+    uint32_t at = kQCol;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j, bd += 1024 >> 4, at += 32)
 #pragma unroll
-    for (int k = 0; k < kLatent / 32; ++k) {
-        const uint64_t bd = sdesc_sw128(c_addr + kSt * kCodes + (k >> 2) * 1024, 16, 4096) + 2 * (k & 3);
-        umma_e4m3_ta(0, kQCol + 8 * k, bd, kIdescS8, k > 0 ? 1u : 0u);
-        umma_e4m3_ta(0, kQCol + 128 + 8 * k, bd, kIdescS8, 1u);
-    }
-    umma_commit(&sm->k_free[kSt]);
+        for (int k = 0; k < 4; ++k) {
+            umma_e4m3_ta(0, at + 8 * k, bd + 2 * k, kIdescS8, j + k > 0 ? 1u : 0u);
+            umma_e4m3_ta(0, at + 128 + 8 * k, bd + 2 * k, kIdescS8, 1u);
+        }
+    umma_commit(&sm->k_free[st]);
     if (!wait_bar(&sm->k_full[2], parity_rope, a.p.status, &sm->abort)) return false;
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         umma_bf16(kKeys, sdesc_sw128(q_addr, 16, 1024) + 2 * k, sdesc_sw128(r_addr, 16, 1024) + 2 * k, kIdescS, k > 0 ? 1u : 0u);
     umma_commit(&sm->k_free[2]);
-    umma_commit(&sm->s_full[kSt]);
+    umma_commit(&sm->s_full[st]);
     return true;
 }
 
@@ -886,10 +888,12 @@ __device__ void score_mma_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_t
                 break;
             }
             tc_fence_after();
-            if (tile & 1)
-                ok = score_tile_fp8<1>(a, sm, q_addr, c_addr, r_addr, fill1++ & 1, tile & 1);
+            const int st = tile & 1;
+            ok = score_tile_fp8(a, sm, q_addr, c_addr, r_addr, st, (st ? fill1 : fill0) & 1, st);
+            if (st)
+                ++fill1;
             else
-                ok = score_tile_fp8<0>(a, sm, q_addr, c_addr, r_addr, fill0++ & 1, tile & 1);
+                ++fill0;
         }
         if (ok) umma_commit(&sm->q_free);
     }
