@@ -15,17 +15,27 @@
 // the whole tensor memory of an SM, so the CTA that accumulates the output has no
 // room for the logits, and queries (144 KB) with cache rows of both products do
 // not fit one SM's shared memory.  A cluster of two splits the two products:
-//   score CTA (rank 0)  holds the 128 x 576 query tile; streams key blocks (128
-//            rows x 64 dims, 16 KB) through a ring of five; S = Q K^T (N = 128)
-//            into one of four TMEM buffers; eight softmax warps (a row's 128
-//            logits over two threads) keep the running maximum and sum and write
-//            P (bf16) straight into the value CTA's shared memory.
-//   value CTA (rank 1)  streams value blocks (64 rows x 256 dims, 32 KB) through
-//            a ring of five and accumulates O += P V (N = 256) in all 512 TMEM
-//            columns; its eight other warps rescale O when the score CTA raised a
-//            row's reference maximum (rare), and write the result.
+//   score CTA (rank 0)  holds the query tile (latent part in tensor memory, RoPE
+//            part in shared memory); streams keys (128 rows x 192 dims, 48 KB)
+//            through a ring of three; S = Q K^T (N = 128) into one of two TMEM
+//            buffers; eight softmax warps (a row's 128 logits over two threads)
+//            keep the running maximum and sum, stage P (bf16) and copy it into the
+//            value CTA's shared memory.
+//   value CTA (rank 1)  streams values (64 rows x 256 dims, 32 KB) through a ring
+//            of five and accumulates O += P V (N = 256) in all 512 TMEM columns;
+//            its eight other warps rescale O when the score CTA raised a row's
+//            reference maximum (rare), and write the result.
 // Both products have full-rate shapes: 36 x 64 cycles for S and 16 x 128 for O per
-// unit, so the pair is bound by the score CTA at 94% of the two SMs' peak.
+// unit, which would bound the pair at 94% of the two SMs' peak.
+//
+// Measured, one B200 at 1965 MHz: 2048 tokens behind 16384 rows, 64 heads, bf16 3.8
+// ms (1.31 PFLOP/s; 1.1 in a long run, under the power limit): a unit takes some 2900
+// cycles, of which the keys' copies, which have one tile's time to arrive from L2 in,
+// and the MMA thread's waits are what exceeds 2304.  Eight tokens at 32768 rows 97 us
+// from cold caches (302 MB: 60 us of it at 5 TB/s, the rest the first tile's way
+// through the pipeline, the partials and their merge).  32 tokens at up to 24000 FP8
+// rows 177 us: the widening and the copies of 656-byte rows, whose 128-byte pieces
+// straddle lines.
 //
 // Split.  The units of the whole batch, in order, are cut into one equal range
 // per cluster, wherever the cuts fall: a batch of short and long sequences, or a
@@ -64,7 +74,9 @@ constexpr int kPSlot = 4 * kBlk;                 // 128 rows x 128 keys
 constexpr int kBig = kQBytes + 2 * kPSlot + kKStages * kKStage;
 static_assert(kBig == 2 * kPSlot + kVStages * kVStage, "both CTAs fill the same space");
 // Packed FP8 rows, score CTA: two tiles of codes (128 keys x 512 bytes), one of RoPE
-// keys; value CTA: units of 32 keys, codes as they come and widened to fp16.
+// keys; value CTA: units of 32 keys, codes as they come and widened to fp16.  (Whole
+// 656-byte rows copied as they lie and laid out for the MMA by two warps: 210 us where
+// this takes 205, the layout having no second buffer to work ahead in.)
 constexpr int kCodes = 8 * kBlk;
 constexpr int kRawStage = 2 * kBlk, kRawStages = 4;
 constexpr int kHStage = 4 * kBlk, kHStages = 3;
@@ -121,8 +133,9 @@ struct Small {
     int abort;
     int plan_b, plan_rt, plan_k0, plan_active;
     Seq plan_seq;
+    int plan_q1;              // q_begin[plan_b + 1]
     Box plan_box[16];         // of the first key tile
-    long long plan_units, plan_end, plan_total, plan_sum[kThreads / 32];
+    long long plan_units, plan_end, plan_total, plan_first, plan_sum[kThreads / 32];
     int cmd;
     int flags[2][4];          // value CTA: [slot][quadrant] some row's O must be rescaled
     uint32_t key_ok[kSBufs];  // score CTA: [S buffer] bit i: keys 8i..8i+7 are in the pool
@@ -275,7 +288,8 @@ __device__ __forceinline__ Seq make_seq(const TcArgs &a, int q0, int q1, int len
     s.q0 = q0;
     s.n = q1 - q0;
     s.len = len;
-    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.p.n_tok && len >= s.n &&
+    // (a sequence within 1024 rows of int32's end would overflow the sums of positions)
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.p.n_tok && len >= s.n && len < INT_MAX - 1024 &&
                     len <= static_cast<long long>(a.p.max_pages) * a.p.page_rows;
     if (!ok) {
         bad = true;
@@ -395,7 +409,7 @@ __device__ void make_plan(const TcArgs &a, Small *sm, int cluster, bool report) 
             const long long u = units_before(s, a.tok_tile, s.tiles);
             if (start < at + u) {
                 sm->plan_b = b;
-                sm->plan_sum[0] = start - at;  // unit of the sequence
+                sm->plan_first = start - at;  // unit of the sequence
                 break;
             }
             at += u;
@@ -407,7 +421,7 @@ __device__ void make_plan(const TcArgs &a, Small *sm, int cluster, bool report) 
     // kThreads places, twice for long chunks
     if (sm->plan_units > 0) {
         const int b = sm->plan_b;
-        const long long unit = sm->plan_sum[0];
+        const long long unit = sm->plan_first;
         const Seq s = make_seq(a, a.p.q_begin[b], a.p.q_begin[b + 1], a.p.seq_len[b], bad);
         int lo = 0, span = s.tiles;  // the tile is in lo .. lo + span - 1
         if (tid == 0) sm->plan_rt = 0;
@@ -429,7 +443,10 @@ __device__ void make_plan(const TcArgs &a, Small *sm, int cluster, bool report) 
             lo = sm->plan_rt;
         }
         // what every role reads first: looked up here, before the copies load the memory
-        if (tid == 0) sm->plan_seq = s;
+        if (tid == 0) {
+            sm->plan_seq = s;
+            sm->plan_q1 = a.p.q_begin[b + 1];
+        }
         if (tid < kKeys / a.box) sm->plan_box[tid] = find_box(a, s, b, sm->plan_k0 * kKeys + tid * a.box);
     }
 }
@@ -439,7 +456,7 @@ __device__ void make_plan(const TcArgs &a, Small *sm, int cluster, bool report) 
 // loaded while the current one is worked on.
 struct Walk {
     const TcArgs &a;
-    int b, rt, k0, k1, nk, next_q1, next_len;
+    int b, rt, k0, k1, nk, q1, next_q1, next_len;  // q1: q_begin[b + 1]
     long long left;
     Seq s;
     __device__ Walk(const TcArgs &args, const Small *sm) : a(args), left(sm->plan_units) {
@@ -448,10 +465,12 @@ struct Walk {
         rt = sm->plan_rt;
         k0 = sm->plan_k0;
         s = sm->plan_seq;
+        next_q1 = sm->plan_q1;
         prefetch();
         piece();
     }
     __device__ void prefetch() {
+        q1 = next_q1;
         if (b + 1 < a.p.n_seq) {
             next_q1 = a.p.q_begin[b + 2];
             next_len = a.p.seq_len[b + 1];
@@ -473,8 +492,7 @@ struct Walk {
                 return;
             }
             bool bad = false;
-            // an out-of-order q_begin keeps its own pair of borders
-            s = make_seq(a, a.p.q_begin[b], next_q1, next_len, bad);
+            s = make_seq(a, q1, next_q1, next_len, bad);
             rt = 0;
             prefetch();
         }

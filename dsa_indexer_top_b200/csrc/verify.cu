@@ -240,6 +240,7 @@ extern "C" dsa_status dsa_verify_drafts(const dsa_verify *v, void *ws, size_t ws
         ~Pop() { nvtxRangePop(); }
     } pop;
     if (!v || v->n_req < 0 || v->n_draft < 0 || v->n_draft >= INT32_MAX || v->vocab < 1) return DSA_ERR_INVALID;
+    if (v->vocab > (1 << 30)) return DSA_ERR_UNSUPPORTED;
     if (v->dtype != DSA_BF16 && v->dtype != DSA_F32)
         return v->dtype == DSA_FP8_E4M3 ? DSA_ERR_UNSUPPORTED : DSA_ERR_INVALID;
     if (v->t_req_stride < 0 || v->t_row_stride < 0 || v->d_req_stride < 0 || v->d_row_stride < 0)

@@ -638,7 +638,7 @@ dsa_status dsa_write_paged_rows(const dsa_cache_writer *writer, const int32_t *s
  *   block_table    device int32, rows table_stride apart, max_pages entries each
  *   q_begin        device int32 [n_seq + 1], not decreasing, 0 <= .. <= n_tok
  *   seq_len        device int32 [n_seq], >= the sequence's new tokens,
- *                  <= max_pages * page_rows
+ *                  <= max_pages * page_rows, < 2^31 - 1025
  */
 typedef struct {
     int32_t n_seq;
@@ -692,7 +692,7 @@ size_t dsa_paged_mla_workspace_bytes(const dsa_paged_batch *batch, const dsa_mla
  * The comparison and the cumulative weights are taken in float64.
  *   n_req, n_draft   requests; drafts per request (>= 0), the row length of
  *                    draft_tokens and accept_u
- *   vocab, dtype     >= 1; DSA_F32 or DSA_BF16, for target and draft
+ *   vocab, dtype     1 .. 2^30; DSA_F32 or DSA_BF16, for target and draft
  *   target           p: row i of request r at target + r*t_req_stride +
  *                    i*t_row_stride (elements), n_draft + 1 rows
  *   draft            q likewise, n_draft rows; or NULL: drafts chosen greedily,
@@ -702,7 +702,7 @@ size_t dsa_paged_mla_workspace_bytes(const dsa_paged_batch *batch, const dsa_mla
  *   accept_u         float32 [n_req][n_draft];  sample_u  float32 [n_req]; in [0, 1)
  *   tokens           int32 [n_req][n_draft + 1]: the accepted drafts, the drawn
  *                    token, then -1
- *   n_accept         int32 [n_req]: accepted drafts
+ *   n_accept         int32 [n_req]: accepted drafts (outputs must not alias inputs)
  *   ws               at least 256 bytes (status word)
  * Probabilities need not be normalised; values that are negative or not finite
  * count as 0.  Where p_i <= q_i everywhere (rounding), the token is drawn from

@@ -130,6 +130,7 @@ def test_verify_other_statuses():
     call = lambda v, ws=WS, n=BIG: lib.dsa_verify_drafts(ctypes.byref(v), ws, n, None)
     assert lib.dsa_verify_drafts(None, WS, BIG, None) == B.DSA_ERR_INVALID
     assert call(_verify(dtype=B.DSA_FP8_E4M3)) == B.DSA_ERR_UNSUPPORTED
+    assert call(_verify(vocab=(1 << 30) + 1)) == B.DSA_ERR_UNSUPPORTED
     for ws, n in ((None, BIG), (WS + 8, BIG), (WS, 128)):
         assert call(_verify(), ws, n) == B.DSA_ERR_WORKSPACE
     assert call(_verify(n_req=0)) == B.DSA_OK

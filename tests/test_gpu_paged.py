@@ -123,7 +123,7 @@ def test_page_tables_report_bad_input(cuda_ok):
 
 
 # ------------------------------------------------------------------ writer
-@pytest.mark.parametrize("n_tok,page", [(1, 16), (7, 8), (16, 64), (40, 24), (300, 64)])
+@pytest.mark.parametrize("n_tok,page", [(1, 16), (4, 16), (5, 8), (7, 8), (16, 64), (40, 24), (300, 64), (1030, 16)])
 def test_write_paged_rows(cuda_ok, n_tok, page):
     """The oracle's rows at the slots; nothing else written."""
     rng = np.random.default_rng(n_tok)
