@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(kGenThreads) paged_mla_generic_kernel(const Pa
             hi = mid;
     }
     const int b = lo, n = a.q_begin[b + 1] - a.q_begin[b], j = i - a.q_begin[b], len = a.seq_len[b];
-    if (j < 0 || j >= n || len < n || len > static_cast<int64_t>(a.max_pages) * a.page_rows) {
+    if (j < 0 || j >= n || len < n || len >= INT_MAX - 1024 ||
+        len > static_cast<int64_t>(a.max_pages) * a.page_rows) {
         if (tid == 0 && h == 0) report_status(a.status, DSA_ERR_INVALID);
         return;
     }
@@ -272,8 +273,9 @@ __global__ void __launch_bounds__(kGenThreads) paged_mla_generic_kernel(const Pa
             }
         }
         const float mc = fmaxf(m, gen_reduce(x, red, true));
+        // (a logit of -infinity has no weight, also where the block has no other)
         const float al = mc == -INFINITY ? 1.f : expf(m - mc);
-        const float pr = o < 0 ? 0.f : expf(x - mc);
+        const float pr = o < 0 || x == -INFINITY ? 0.f : expf(x - mc);
         l = l * al + gen_reduce(pr, red, false);
         m = mc;
         pw[tid] = pr;
@@ -288,14 +290,14 @@ __global__ void __launch_bounds__(kGenThreads) paged_mla_generic_kernel(const Pa
         }
     }
     const int64_t oo = (static_cast<int64_t>(i) * a.heads + h) * a.d_lat;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
     for (int d = tid; d < a.d_lat; d += kGenThreads) {
         if (kKind == 0)
             static_cast<float *>(a.out)[oo + d] = acc[d] * inv;
         else
             static_cast<__nv_bfloat16 *>(a.out)[oo + d] = __float2bfloat16_rn(acc[d] * inv);
     }
-    if (tid == 0 && a.lse) a.lse[static_cast<int64_t>(i) * a.heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    if (tid == 0 && a.lse) a.lse[static_cast<int64_t>(i) * a.heads + h] = l != 0.f ? m + logf(l) : -INFINITY;
 }
 
 constexpr int kGenMaxDims = 8192;  // d_lat + d_rope of the CUDA-core kernel: shared memory of the launch

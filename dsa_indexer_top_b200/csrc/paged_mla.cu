@@ -96,6 +96,7 @@ constexpr float kRescale = 32.0f;
 // rounded to fp16's smallest step only 2^-28 under it.
 constexpr float kRescaleFp8 = 10.0f;
 constexpr float kShiftFp8 = 4.0f;
+constexpr uint32_t kNoRow = 0x80000000u;         // scale of a row nobody sees
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kIdescS = idesc_bf16(128, 128, false, false);
@@ -137,12 +138,13 @@ struct Small {
     Box plan_box[16];         // of the first key tile
     long long plan_units, plan_end, plan_total, plan_first, plan_sum[kThreads / 32];
     int cmd;
-    int flags[2][4];          // value CTA: [slot][quadrant] some row's O must be rescaled
+    int flags[2][4];          // value CTA: [slot][quadrant] 1: some row's O must be rescaled; 2: clean the values
     uint32_t key_ok[kSBufs];  // score CTA: [S buffer] bit i: keys 8i..8i+7 are in the pool
     union {
         struct alignas(16) {  // (the scales are read 16 bytes at a time)
             float sigma[2][kKeys];      // score CTA: [tile parity] row scales
             uint16_t xmax[2][2][kRows];  // [tile parity][half][row] maxima, bf16
+            int nf[2][4];               // [tile parity][quadrant] the upper half has a logit that is not finite
         } q;
         struct {
             float alpha[2][kRows];  // value CTA: [slot][row]
@@ -161,6 +163,7 @@ struct TcArgs {
     PagedMlaArgs p;
     int clusters;
     int tok_tile;       // tokens per row tile
+    int max_len;        // rows of a block-table row; 1025 short of int32's end, for the sums of positions
     int box;            // rows per TMA copy (divides page_rows, 8..64)
     Meta *meta;         // [clusters]
     float *part_ml;     // [2 * clusters][2][128] maximum (log2), sum
@@ -288,9 +291,7 @@ __device__ __forceinline__ Seq make_seq(const TcArgs &a, int q0, int q1, int len
     s.q0 = q0;
     s.n = q1 - q0;
     s.len = len;
-    // (a sequence within 1024 rows of int32's end would overflow the sums of positions)
-    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.p.n_tok && len >= s.n && len < INT_MAX - 1024 &&
-                    len <= static_cast<long long>(a.p.max_pages) * a.p.page_rows;
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.p.n_tok && len >= s.n && len <= a.max_len;
     if (!ok) {
         bad = true;
         s.n = 0;
@@ -810,7 +811,8 @@ __device__ void score_producer_fp8(const TcArgs &a, Small *sm, uint8_t *q_sm, ui
 }
 
 // Row scales of every key tile to shared memory, divided by the tile's largest power
-// of two; 0 for a row nobody sees.
+// of two; -0 for a row nobody sees (a visible row may well have scale 0: its latent
+// part is zero, its RoPE part still counts).
 __device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
     const int lane = threadIdx.x & 31;
     uint32_t tile = 0;
@@ -819,23 +821,32 @@ __device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
         for (int kt = w.k0; kt < w.k1; ++kt, ++tile) {
             const int s0 = kt * kKeys + 4 * lane;
             float v[4] = {0.f, 0.f, 0.f, 0.f};
+            int seen = 0;
             const Box x = find_box(a, w.s, w.b, s0);  // (four rows of one 8-row group)
             if (x.page < a.p.n_pages) {
                 const uint8_t *row = kv + x.page * a.p.kv_page_stride + (8 * x.group + (s0 & 7)) * a.p.kv_row_stride;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (s0 + i < w.s.len) v[i] = __ldg(reinterpret_cast<const float *>(row + i * a.p.kv_row_stride));
+                    if (s0 + i < w.s.len) {
+                        v[i] = __ldg(reinterpret_cast<const float *>(row + i * a.p.kv_row_stride));
+                        ++seen;
+                    }
             }
-            float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-            const bool gap = __any_sync(0xffffffffu, !(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])) > 0.f));
+            float mx = 0.f;  // (of the finite ones: a token need not see the others)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[i]) <= FLT_MAX ? fabsf(v[i]) : 0.f);
+            const bool gap = __any_sync(0xffffffffu, seen < 4);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-            e = mx > 0.f ? min(max(e, -120), 120) : 0;
+            // (2^-e multiplies a row's sum, which has to stay finite: no less than -80)
+            e = mx > 0.f ? min(max(e, -80), 120) : 0;
             const float down = u2f(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = i < seen ? v[i] * down + 0.f : -0.f;
             if (tile >= 2 && !wait_bar(&sm->sig_free[tile & 1], (tile / 2 - 1) & 1, a.p.status, &sm->abort)) return;
             *reinterpret_cast<float4 *>(&sm->q.sigma[tile & 1][4 * lane]) =
-                make_float4(v[0] * down, v[1] * down, v[2] * down, v[3] * down);
+                make_float4(v[0], v[1], v[2], v[3]);
             if (lane == 0) {
                 sm->sig_exp[tile & 1] = e;
                 sm->sig_gap[tile & 1] = gap;
@@ -999,12 +1010,25 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->s_free[sbuf]);
             float mx = -INFINITY;
+            // some logit is not finite, in a tile of tokens that do not see the same rows: the
+            // row's values may be NaN, and 0 x NaN is NaN for those that do not see it (see
+            // clean_stage)
+            bool nf = false;
+            const int s0 = kt * kKeys + 64 * half;
             if (used) {
-                const int s0 = kt * kKeys + 64 * half;
                 if (s0 + 63 > pos0 || gap) {
+                    float z4[4] = {0.f, 0.f, 0.f, 0.f};  // NaN where a logit is not finite
+                    if (kFp8 && pos0 < w.s.len - 1) {    // (in the loop below it would spill)
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (s0 + i > pos || (kFp8 ? !(sig[i] > 0.f) : !((okbits >> (i / 8)) & 1))) x[i] = 0xFF800000u;
+                        for (int i = 0; i < 64; ++i) z4[i & 3] = fmaf(u2f(x[i]), 0.f, z4[i & 3]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        if (!kFp8) z4[i & 3] = fmaf(u2f(x[i]), 0.f, z4[i & 3]);
+                        if (s0 + i > pos || (kFp8 ? __float_as_uint(sig[i]) == kNoRow : !((okbits >> (i / 8)) & 1)))
+                            x[i] = 0xFF800000u;
+                    }
+                    nf = __any_sync(0xffffffffu, r < rows && pos0 < w.s.len - 1 && !((z4[0] + z4[1]) + (z4[2] + z4[3]) == 0.f));
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1019,6 +1043,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             float al = 1.f;
             if (live) {
                 sm->q.xmax[slot][half][r] = static_cast<uint16_t>(__float_as_uint(mx) >> 16);
+                if (half == 1 && lane == 0) sm->q.nf[slot][quad] = nf;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
                 if (!wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) {
@@ -1026,6 +1051,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                     break;
                 }
                 xphase ^= 1;
+                if (half == 0) nf |= sm->q.nf[slot][quad] != 0;
                 mx = fmaxf(mx, u2f(static_cast<uint32_t>(sm->q.xmax[slot][half ^ 1][r]) << 16));
                 if (m == -INFINITY) {
                     m = mx;  // nothing accumulated for the row yet
@@ -1069,6 +1095,12 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                 }
                 const float lt = (l4[0] + l4[1]) + (l4[2] + l4[3]);
                 l += kFp8 ? lt * ex2(-te) : lt;
+                if (kFp8 && nf) {  // (a scale that is not finite)
+#pragma unroll 1
+                    for (int i = 0; i < 64; ++i)
+                        if (s0 + i > pos || __float_as_uint(sig[i]) == kNoRow)
+                            *reinterpret_cast<uint16_t *>(pl + sw128_offset(r, i >> 3) + 2 * (i & 7)) = 0;
+                }
             }
             fence_proxy_async_smem();
             if (kFp8) {
@@ -1086,7 +1118,8 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             }
             if (half == 0) {
                 if (flag) st_remote(r_alpha + (slot * kRows + r) * 4, __float_as_uint(al), r_pfull + slot * 8);
-                if (lane == 0) st_remote(r_flags + (slot * 4 + quad) * 4, flag ? 1u : 0u, r_pfull + slot * 8);
+                if (lane == 0)
+                    st_remote(r_flags + (slot * 4 + quad) * 4, (flag ? 1u : 0u) | (nf ? 2u : 0u), r_pfull + slot * 8);
             }
             __syncwarp();
             if (lane == 0) {
@@ -1218,6 +1251,27 @@ __device__ __forceinline__ bool post_command(const TcArgs &a, Small *sm, int cmd
     return !wait || wait_bar(&sm->cmd_done, ph, a.p.status, &sm->abort);
 }
 
+// A stage's values that are not finite (an exponent of all ones) become zeros.  For
+// the tiles in which some token does not see such a row: the tokens that do see it
+// have NaN weights there, from a logit that is NaN or infinite as well.  One warp, some
+// 5 us a tile: the rows of a sound cache never come here.
+__device__ __forceinline__ void clean_stage(uint8_t *v, int lane, uint32_t expo) {
+#pragma unroll 1
+    for (int i = lane; i < 4 * kBlk / 16; i += 32) {
+        uint4 x = reinterpret_cast<uint4 *>(v)[i];
+        uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t e = w[k] & expo;
+            if ((e & 0xFFFFu) == (expo & 0xFFFFu)) w[k] &= 0xFFFF0000u;
+            if ((e >> 16) == (expo >> 16)) w[k] &= 0x0000FFFFu;
+        }
+        reinterpret_cast<uint4 *>(v)[i] = x;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 template <bool kFp8>
 __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_sm) {
     const int lane = threadIdx.x & 31;
@@ -1237,7 +1291,8 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
             if (lane == 0) arrive_remote(map_rank(smem_u32(&sm->p_got[slot]), 0));
             tc_fence_after();
             const volatile int *fl = sm->flags[slot];
-            if (fl[0] | fl[1] | fl[2] | fl[3]) {
+            const int todo = fl[0] | fl[1] | fl[2] | fl[3];
+            if (todo & 1) {
                 uint32_t good = 1;
                 if (lane == 0) good = post_command(a, sm, kCmdRescale + (slot << 8), cphase, true) ? 1u : 0u;
                 good = __shfl_sync(0xffffffffu, good, 0);
@@ -1256,6 +1311,7 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
                         ok = false;
                         break;
                     }
+                    if (todo & 2) clean_stage(v_sm + st * kHStage, lane, 0x7C007C00u);
                     if (lane == 0) {
                         tc_fence_after();
                         const uint64_t hd = sdesc_sw128(smem_u32(v_sm), 1024, 8192);
@@ -1290,6 +1346,7 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
+                if (todo & 2) clean_stage(v_sm + st * kVStage, lane, 0x7F807F80u);
                 if (lane == 0) {
                     tc_fence_after();
 #pragma unroll
@@ -1409,7 +1466,7 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
         if ((cmd & 255) == kCmdExit) break;
         if ((cmd & 255) == kCmdRescale) {
             const int slot = cmd >> 8;
-            if (*reinterpret_cast<volatile int *>(&sm->flags[slot][quad])) {
+            if (*reinterpret_cast<volatile int *>(&sm->flags[slot][quad]) & 1) {
                 const float al = sm->v.alpha[slot][r];
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 32) {
@@ -1427,7 +1484,7 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
             const int rows = w.rows();
             const bool live = r < rows;
             const float l = sm->v.l[r], m = sm->v.m[r];
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l != 0.f ? 1.f / l : 0.f;
             const bool whole = w.k0 == 0 && w.k1 == w.nk;
             const int64_t row = w.row0() + r;
             const int64_t pslot = 2 * cluster + (w.k0 == 0 ? 1 : 0);
@@ -1475,7 +1532,7 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
                     a.part_ml[pslot * 2 * kRows + r] = m;
                     a.part_ml[(pslot * 2 + 1) * kRows + r] = l;
                 } else if (a.p.lse) {
-                    a.p.lse[row] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+                    a.p.lse[row] = l != 0.f ? m * kLn2 + logf(l) : -INFINITY;
                 }
             }
             if (tid == 0 && w.k0 == 0 && w.k1 < w.nk) {
@@ -1698,9 +1755,9 @@ __global__ void __launch_bounds__(256) paged_mla_merge_kernel(const TcArgs a) {
         if ((i & 7) == warp) wt[i][lane] = w;
         L += w * l;
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L != 0.f ? 1.f / L : 0.f;
     if (warp == 0 && blockIdx.z == 0 && r < me.rows && a.p.lse)
-        a.p.lse[static_cast<int64_t>(me.row0) + r] = L > 0.f ? M * kLn2 + logf(L) : -INFINITY;
+        a.p.lse[static_cast<int64_t>(me.row0) + r] = L != 0.f ? M * kLn2 + logf(L) : -INFINITY;
     __syncthreads();
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -1759,6 +1816,7 @@ cudaError_t launch_paged_mla_tc(const PagedMlaArgs &p, void *scratch, int num_sm
     a.p = p;
     a.clusters = tc_clusters(num_sms);
     a.tok_tile = kRows / p.heads;
+    a.max_len = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.max_pages) * p.page_rows, INT_MAX - 1025));
     a.box = 64;
     while (p.page_rows % a.box != 0) a.box >>= 1;
     const int64_t rows = static_cast<int64_t>(p.n_tok) * p.heads;

@@ -250,6 +250,12 @@ extern "C" dsa_status dsa_verify_drafts(const dsa_verify *v, void *ws, size_t ws
     const uintptr_t el = v->dtype == DSA_F32 ? 3 : 1;
     if ((reinterpret_cast<uintptr_t>(v->target) & el) || (reinterpret_cast<uintptr_t>(v->draft) & el))
         return DSA_ERR_INVALID;
+    const bool any = v->n_draft > 0;  // (empty arrays may stand anywhere)
+    const void *in[] = {v->target,   v->sample_u, v->draft_len, any ? v->draft : nullptr, any ? v->draft_tokens : nullptr,
+                        any ? v->accept_u : nullptr};
+    for (const void *x : in)
+        if (x && v->n_req > 0 && (x == v->tokens || x == v->n_accept)) return DSA_ERR_INVALID;
+    if (v->n_req > 0 && static_cast<const void *>(v->tokens) == v->n_accept) return DSA_ERR_INVALID;
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < 256) return DSA_ERR_WORKSPACE;
     if (v->n_req == 0) return DSA_OK;
     dsa::VerifyArgs a;

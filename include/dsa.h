@@ -667,15 +667,17 @@ typedef struct {
  *         bytes).  Heads: 1 or more.
  *   ws    dsa_paged_mla_workspace_bytes(batch, mla) bytes, 256-byte aligned
  * Output rows outside [q_begin[0], q_begin[n_seq]) are left as they were.  Pool
- * rows at or past a sequence's seq_len may hold anything, NaN included.  A token
- * that sees no row (every page missing) gives 0 and an lse of -infinity.
+ * rows at or past a sequence's seq_len may hold anything, NaN included, and a row
+ * that is not finite reaches the tokens that see it only.  A token that sees no row
+ * (every page missing) gives 0 and an lse of -infinity.
  * Device-detected errors set DSA_ERR_INVALID in the status word: a sequence whose
  * q_begin or seq_len is out of range is skipped, a page outside the pool counts
  * as rows nobody sees.
  * Paths: bf16 queries with up to 128 heads x (512 + 64) over bf16 or packed FP8
- * rows run on tcgen05 tensor cores when page_rows is a multiple of 8 and the pool
- * is aligned as dsa_mla asks, its page stride a whole number of rows; other bf16
- * and float32 shapes run a CUDA-core kernel.
+ * rows run on tcgen05 tensor cores when page_rows is a multiple of 8, the scale is
+ * positive and q, out, kv and the pool's strides are multiples of 16 bytes; other
+ * bf16 and float32 shapes (up to 8192 dims, 65535 heads) run a CUDA-core kernel.
+ * Calls that run at the same time need workspaces of their own.
  */
 dsa_status dsa_paged_mla(const dsa_paged_batch *batch, const dsa_mla *mla, void *ws, size_t ws_bytes, void *stream);
 size_t dsa_paged_mla_workspace_bytes(const dsa_paged_batch *batch, const dsa_mla *mla);
@@ -702,7 +704,8 @@ size_t dsa_paged_mla_workspace_bytes(const dsa_paged_batch *batch, const dsa_mla
  *   accept_u         float32 [n_req][n_draft];  sample_u  float32 [n_req]; in [0, 1)
  *   tokens           int32 [n_req][n_draft + 1]: the accepted drafts, the drawn
  *                    token, then -1
- *   n_accept         int32 [n_req]: accepted drafts (outputs must not alias inputs)
+ *   n_accept         int32 [n_req]: accepted drafts (outputs must not alias inputs:
+ *                    DSA_ERR_INVALID for the same pointer)
  *   ws               at least 256 bytes (status word)
  * Probabilities need not be normalised; values that are negative or not finite
  * count as 0.  Where p_i <= q_i everywhere (rounding), the token is drawn from

@@ -119,7 +119,8 @@ def _verify(**kw):
 @pytest.mark.parametrize("kw", [
     dict(n_req=-1), dict(n_draft=-1), dict(vocab=0), dict(dtype=5), dict(target=None), dict(target=0x1002),
     dict(draft=0x2001), dict(draft_tokens=None), dict(accept_u=None), dict(sample_u=None), dict(tokens=None),
-    dict(n_accept=None), dict(t_req_stride=-1), dict(t_row_stride=-1), dict(d_req_stride=-1), dict(d_row_stride=-1)])
+    dict(n_accept=None), dict(t_req_stride=-1), dict(t_row_stride=-1), dict(d_req_stride=-1), dict(d_row_stride=-1),
+    dict(tokens=0x3000), dict(tokens=0x1000), dict(n_accept=0x4000), dict(n_accept=0x6000)])
 def test_verify_rejects(kw):
     v = _verify(**kw)
     assert B.lib().dsa_verify_drafts(ctypes.byref(v), WS, BIG, None) == B.DSA_ERR_INVALID

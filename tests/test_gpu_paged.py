@@ -233,7 +233,8 @@ class Case:
         assert B.dsa_check_status(self.ws) == status
         return self
 
-    def check(self, table=None, total=None, skip=()):
+    def check(self, table=None, total=None, skip=(), nan=(), any_value=()):
+        """skip: sequences left alone; nan: tokens whose row is NaN; any_value: tokens not compared."""
         table = self.table if table is None else table
         q = self.q.double().cpu().numpy()
         want, lse, touched = P.paged_mla(q, self.rows, table, self.begin, self.total, self.page, self.d_lat, self.scale)
@@ -242,13 +243,18 @@ class Case:
             touched[self.begin[b]:self.begin[b + 1]] = False
         got = self.out.double().cpu().numpy()
         assert (got[~touched] == 77).all(), "rows outside the sequences were written"
+        left = ~touched
+        for i in nan:
+            assert np.isnan(got[i]).all()
+            assert self.lse is None or torch.isnan(self.lse[i]).all()
+        touched[list(nan) + list(any_value)] = False
         half = 2.0 ** -24 if self.kind == "f32" else 2.0 ** -8
         tol = half * np.abs(want) + (2.1e-3 + (0 if self.kind == "f32" else 2.0 ** -8)) * mag + 1e-6
         err = np.abs(got - want)[touched] / tol[touched]
         assert np.isfinite(got[touched]).all() and err.max(initial=0) <= 1, f"{err.max():.3f} of the tolerance"
         if self.lse is not None:
             gl = self.lse.double().cpu().numpy()
-            assert (gl[~touched] == 77).all()
+            assert (gl[left] == 77).all()
             seen = np.isfinite(lse) & touched[:, None]
             assert (np.abs(gl[seen] - lse[seen]) <= 1e-3).all()
             assert (gl[touched[:, None] & ~np.isfinite(lse)] == -np.inf).all()
@@ -324,6 +330,59 @@ def test_attention_missing_pages(cuda_ok, kind):
     c.table[1, :] = -1
     c.batch.block_table = _i32(c.table)
     c.run(B.DSA_ERR_INVALID).check()
+
+
+@pytest.mark.parametrize("kind,what", [("bf16", "nan"), ("bf16", "inf"), ("f32", "nan"), ("fp8", "nan"),
+                                       ("fp8", "scale nan"), ("fp8", "scale inf")])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_attention_later_rows_that_are_not_finite(cuda_ok, kind, what, heads):
+    """A row with NaN or infinities is NaN in the tokens that see it and nothing in those before it."""
+    seqs = [(100, 7), (0, 3), (126, 4), (1500, 20), (300, 1)]
+    where = [103, 1, 128, 1500, None]                # the row of each sequence
+    shape = dict(d_lat=64, d_rope=16) if kind == "f32" else {}
+    c = Case(seqs, heads=heads, page=16, kind=kind, seed=13, **shape)
+    nan = []
+    for b, s in enumerate(where):
+        if s is None:
+            continue
+        at = c.table[b, s // 16], s % 16
+        c.rows[at] = 0
+        if kind != "fp8":
+            c.pool[at][5:8] = float("nan") if what == "nan" else float("inf")
+        elif what == "nan":
+            c.pool[at][5:8] = 0x7F
+        else:
+            c.pool[at][640:644] = torch.tensor([float(what.split()[1])], device=DEV).view(torch.uint8)
+        nan += range(int(c.begin[b]) + s - c.ctx[b], int(c.begin[b + 1]))
+    # (an infinite row's logit may also be -infinity)
+    c.run().check(**{"nan" if "nan" in what else "any_value": nan})
+
+
+@pytest.mark.parametrize("heads", [8, 64])
+def test_attention_fp8_rows_without_latent_part(cuda_ok, heads):
+    """A scale of zero: the latent part is zero, the RoPE part counts; scales far apart."""
+    c = Case([(300, 1), (128, 2), (200, 5), (20, 1)], heads=heads, page=16, kind="fp8", seed=14)
+    for b, rows in enumerate([[0, 5, 130, 299, 300], list(range(130)), [203, 7], list(range(21))]):
+        for s in rows:
+            at = c.table[b, s // 16], s % 16
+            # scale 0; every other row 2^-60 of what it was
+            f = 0.0 if s % 2 or b == 3 else 2.0 ** -60
+            c.pool[at][640:644] = (c.pool[at][640:644].view(torch.float32) * f).view(torch.uint8)
+            c.rows[at][:512] *= f
+    c.run().check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_attention_lengths_at_the_end_of_int32(cuda_ok, kind):
+    """Positions past int32's end are refused; nothing of that sequence is read or written."""
+    shape = dict(d_lat=64, d_rope=16) if kind == "f32" else {}
+    c = Case([(30, 2), (40, 1)], heads=4, page=16, kind=kind, seed=15, **shape)
+    wide = torch.zeros(2, (1 << 27) + 1, dtype=torch.int32, device=DEV)   # page 0 wherever it is read
+    wide[:, :c.table.shape[1]] = _i32(c.table)
+    c.batch.block_table = wide
+    for length in (2 ** 31 - 1, 2 ** 31 - 1025):
+        c.batch.seq_len = _i32([length, 41])
+        c.run(B.DSA_ERR_INVALID).check(skip=[0])
 
 
 def test_attention_bad_sequences_are_skipped(cuda_ok):
