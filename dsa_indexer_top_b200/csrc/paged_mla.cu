@@ -28,14 +28,14 @@
 // Both products have full-rate shapes: 36 x 64 cycles for S and 16 x 128 for O per
 // unit, which would bound the pair at 94% of the two SMs' peak.
 //
-// Measured, one B200 at 1965 MHz: 2048 tokens behind 16384 rows, 64 heads, bf16 3.8
-// ms (1.31 PFLOP/s; 1.1 in a long run, under the power limit): a unit takes some 2900
-// cycles, of which the keys' copies, which have one tile's time to arrive from L2 in,
-// and the MMA thread's waits are what exceeds 2304.  Eight tokens at 32768 rows 97 us
-// from cold caches (302 MB: 60 us of it at 5 TB/s, the rest the first tile's way
-// through the pipeline, the partials and their merge).  32 tokens at up to 24000 FP8
-// rows 177 us: the widening and the copies of 656-byte rows, whose 128-byte pieces
-// straddle lines.
+// Measured (one B200, cold caches, merge included).  2048 tokens behind 16384 rows, 64
+// heads, bf16: 3.9 ms (1.27 PFLOP/s), 4.5 in a long run under the power limit; a unit
+// takes some 2900 cycles, and what exceeds 2304 is the keys' copies, which have one
+// tile's time to arrive from L2 in, and the MMA thread's waits.  Eight tokens at 32768
+// rows: 98 us (302 MB: 60 us of it at 5 TB/s, the rest the first tile's way through the
+// pipeline, the partials and their merge).  32 tokens at up to 24000 packed FP8 rows:
+// 182 us (215 MB): one S buffer, the widening, instruction fetch, and copies of
+// 656-byte rows, whose 128-byte pieces straddle lines.
 //
 // Split.  The units of the whole batch, in order, are cut into one equal range
 // per cluster, wherever the cuts fall: a batch of short and long sequences, or a
@@ -83,7 +83,7 @@ constexpr int kHStage = 4 * kBlk, kHStages = 3;
 static_assert(kBig == kQBytes + 2 * kPSlot + 2 * kCodes + 2 * kBlk, "shared memory, FP8 score CTA");
 static_assert(kBig == 2 * kPSlot + kRawStages * kRawStage + kHStages * kHStage, "shared memory, FP8 value CTA");
 constexpr int kSmemMax = 232448;                 // 227 KB
-constexpr int kThreads = 384;                    // 8 softmax / output warps; producer, MMA, 2 idle
+constexpr int kThreads = 384;                    // 8 softmax / output warps, producer, MMA; FP8: row scales; idle
 constexpr int kSBufs = 2;
 constexpr int kQCol = kSBufs * kKeys;            // TMEM column of the query blocks, 32 columns each
 static_assert(kQCol + 32 * kQTmem <= 512, "tensor memory");
@@ -509,7 +509,7 @@ struct Walk {
 
 // Copies of cache rows land as [8-row group][64-dim block][8 rows][128 bytes], a
 // swizzle atom per (group, block): a run of blocks of a whole page comes with one
-// instruction (each costs the issuing thread some 80 cycles), and both products'
+// instruction (each costs the issuing warp some 300 cycles), and both products'
 // descriptors take the strides between groups and blocks.
 __device__ __forceinline__ void tma_load_rows(void *dst, const CUtensorMap *map, uint64_t *bar, int block, const Box &x) {
     asm volatile(
@@ -633,9 +633,10 @@ __device__ void score_producer(const TcArgs &a, Small *sm, uint8_t *q_sm, uint8_
 }
 
 // One unit's 36 MMAs into S buffer buf.  Tensor memory is allocated whole, so its
-// base is 0 and every address and descriptor here is a constant: an operand that
-// has to be moved to a uniform register first costs the issuing thread more than
-// the 64 cycles an MMA takes (measured: 115 cycles per MMA with a computed stage).
+// base is 0 and the query's columns and the stages' descriptors follow from one base
+// each; only the S buffer's column changes from tile to tile.  One body for both
+// buffers: with a copy of it for each, the MMAs waited for instructions (an MMA of this
+// shape takes 64 cycles and its issue some 60).
 // A tile of 64 keys or fewer multiplies what an earlier tile left in the upper
 // half too; those columns are not read.
 __device__ __forceinline__ bool score_tile(const TcArgs &a, Small *sm, uint32_t q_addr, uint32_t k_addr, uint32_t parity,
