@@ -271,6 +271,32 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two float32 operations in one instruction (a, b as pairs in one 64-bit register).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -962,7 +988,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         const int tok = w.rt * a.tok_tile + min(r, rows - 1) / a.p.heads;
         const int pos = w.s.len - w.s.n + tok;
         const int pos0 = w.s.len - w.s.n + w.rt * a.tok_tile;  // the tile's first token
-        const float qc2 = kFp8 ? c2 * a.q8_scale[w.row0() + min(r, rows - 1)] : 0.f;
+        const float q8s = kFp8 ? a.q8_scale[w.row0() + min(r, rows - 1)] : 0.f;
         float m = -INFINITY, l = 0.f;
         for (int kt = w.k0; kt < w.k1; ++kt, ++tile) {
             const uint32_t slot = tile & 1;  // of P, and of bf16's S buffers
@@ -988,8 +1014,8 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                     tmem_ld32(tb + kKeys * slot + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
                     tmem_ld_wait();
                 } else {
-                    // log2 of the weight: c2 (s sigma S_lat + S_rope)
-                    const float qs = qc2 * ex2(te);
+                    // logit over the scale: s sigma S_lat + S_rope
+                    const float qs = q8s * ex2(te);
 #pragma unroll
                     for (int c = 0; c < 64; c += 32) {
                         uint32_t y[32];
@@ -999,10 +1025,16 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             const float4 g4 = *reinterpret_cast<const float4 *>(sig + c + i);
-                            const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+                            const uint64_t g[2] = {pair(g4.x, g4.y), pair(g4.z, g4.w)};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                x[c + i + k] = __float_as_uint(fmaf(u2f(x[c + i + k]) * g[k], qs, u2f(y[i + k]) * c2));
+                            for (int k = 0; k < 2; ++k) {
+                                const int e = c + i + 2 * k;
+                                const float2 z =
+                                    unpair(fma2(mul2(pair(u2f(x[e]), u2f(x[e + 1])), g[k]), pair(qs, qs),
+                                                pair(u2f(y[i + 2 * k]), u2f(y[i + 2 * k + 1]))));
+                                x[e] = __float_as_uint(z.x);
+                                x[e + 1] = __float_as_uint(z.y);
+                            }
                         }
                     }
                 }
@@ -1039,7 +1071,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 // (the running maximum is of the weight times the tile's power of two, which
                 // bounds what the MMA gets)
-                mx = bf16_up(kFp8 ? mx + te : mx * c2);  // (scale > 0)
+                mx = bf16_up(fmaf(mx, c2, te));  // (scale > 0)
             }
             float al = 1.f;
             if (live) {
@@ -1070,21 +1102,29 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             }
             if (used) {
                 const float mu = (m == -INFINITY ? 0.f : m) - (kFp8 ? kShiftFp8 + te : 0.f);
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t c22 = pair(c2, c2), mu2 = pair(-mu, -mu);
+                uint64_t l2[2] = {0, 0};
                 uint8_t *pl = p_stage + slot * kPSlot + half * 2 * kBlk;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     float p[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        p[i] = kFp8 ? ex2(u2f(x[8 * c + i]) - mu) : ex2(fmaf(u2f(x[8 * c + i]), c2, -mu));
-                        l4[i & 3] += p[i];
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 z = unpair(fma2(pair(u2f(x[8 * c + i]), u2f(x[8 * c + i + 1])), c22, mu2));
+                        p[i] = ex2(z.x);
+                        p[i + 1] = ex2(z.y);
+                        l2[(i / 2) & 1] = add2(l2[(i / 2) & 1], pair(p[i], p[i + 1]));
                     }
                     if constexpr (kFp8) {
                         const float4 ga = *reinterpret_cast<const float4 *>(sig + 8 * c);
                         const float4 gb = *reinterpret_cast<const float4 *>(sig + 8 * c + 4);
-                        p[0] *= ga.x, p[1] *= ga.y, p[2] *= ga.z, p[3] *= ga.w;
-                        p[4] *= gb.x, p[5] *= gb.y, p[6] *= gb.z, p[7] *= gb.w;
+                        const uint64_t g[4] = {pair(ga.x, ga.y), pair(ga.z, ga.w), pair(gb.x, gb.y), pair(gb.z, gb.w)};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 z = unpair(mul2(pair(p[2 * i], p[2 * i + 1]), g[i]));
+                            p[2 * i] = z.x;
+                            p[2 * i + 1] = z.y;
+                        }
                     }
                     // bf16 (fp16) weights for the MMA; the sum keeps the float32 values, so the
                     // roundings (half a step, 2^-8 relative) average out in the output
@@ -1094,7 +1134,8 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                              : make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
                                           pack_bf16(p[6], p[7]));
                 }
-                const float lt = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                const float2 ls = unpair(add2(l2[0], l2[1]));
+                const float lt = ls.x + ls.y;
                 l += kFp8 ? lt * ex2(-te) : lt;
                 if (kFp8 && nf) {  // (a scale that is not finite)
 #pragma unroll 1
