@@ -435,6 +435,90 @@ def test_attention_second_call_stream_and_graph(cuda_ok):
     c.check()
 
 
+def test_attention_calls_at_the_same_time(cuda_ok):
+    """Calls on three streams, each with a workspace of its own, give what they give alone."""
+    cases = [Case([(900, 1), (3000, 2), (70, 40)], heads=64, page=16, kind=k, seed=16 + i)
+             for i, k in enumerate(["bf16", "fp8", "bf16"])]
+    alone = [c.run().out.clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(4):
+        for c in cases:
+            c.out.fill_(77.0)
+        torch.cuda.synchronize()
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                B.dsa_paged_mla(c.batch, c.mla, c.ws)
+        torch.cuda.synchronize()
+        for c, want in zip(cases, alone):
+            assert B.dsa_check_status(c.ws) == B.DSA_OK and torch.equal(c.out, want)
+
+
+def test_attention_two_graphs_share_a_workspace(cuda_ok):
+    """Two captured calls over one workspace, replayed in turn on one stream."""
+    a = Case([(2000, 1), (31, 2)], heads=64, page=16, kind="fp8", seed=19).run().check()
+    b = Case([(5, 60), (1100, 1), (64, 1)], heads=16, page=32, seed=20).run().check()
+    ws = a.ws if a.ws.numel() >= b.ws.numel() else b.ws
+    want = [a.out.clone(), b.out.clone()]
+    graphs = []
+    for c in (a, b):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            B.dsa_paged_mla(c.batch, c.mla, ws)
+    for _ in range(3):
+        a.out.fill_(77.0)
+        b.out.fill_(77.0)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert B.dsa_check_status(ws) == B.DSA_OK
+        assert torch.equal(a.out, want[0]) and torch.equal(b.out, want[1])
+
+
+def test_tables_and_rows_captured(cuda_ok):
+    """Tables and rows in one graph, replayed on other lengths: rows at the new slots."""
+    rng = np.random.default_rng(22)
+    page, n_tok, H = 16, 40, 256
+    ctx, new = np.array([30, 0, 7]), np.array([9, 20, 3])
+    held, table, free, n_pages = _layout(rng, ctx, new, page)
+    free = np.concatenate([free, free])                     # (room for either step's pages)
+    table = np.concatenate([table, np.full((3, 2), -1)], 1)
+    p = _plan(ctx, new, held, table, free, 0, page, n_pages, n_tok)
+    g = torch.Generator(device=DEV).manual_seed(22)
+    rn = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    h, w = rn(n_tok, H).bfloat16(), (rn(704, H) / H ** 0.5).bfloat16()
+    norms = (1 + 0.1 * rn(512), 1 + 0.1 * rn(128), 0.1 * rn(128))
+    kv = torch.empty(n_pages, page, 576, dtype=torch.bfloat16, device=DEV)
+    ws = torch.zeros(max(256, B.dsa_cache_writer_workspace_bytes(n_tok, H)), dtype=torch.uint8, device=DEV)
+    writer = B.CacheWriter(h, w, *norms, None, p.q_pos, kv, None)
+
+    def step():
+        B.dsa_page_tables(p, ws)
+        B.dsa_write_paged_rows(writer, p.slot_map, ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for c2, n2 in ((ctx, new), (ctx - [1, 0, 7], np.array([2, 1, 31]))):
+        p.ctx_len.copy_(_i32(c2))
+        p.new_len.copy_(_i32(n2))
+        p.block_table.copy_(_i32(table))
+        kv.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert B.dsa_check_status(ws) == B.DSA_OK
+        want = P.page_tables(c2, n2, held, free, 0, table, page, n_tok)
+        for k in CHECKS:
+            np.testing.assert_array_equal(getattr(p, k).cpu().numpy(), want[k], err_msg=k)
+        rows = PR.latent_rows(h.float().cpu().numpy(), w[:576].float().cpu().numpy().T, norms[0].cpu().numpy(), want["q_pos"])
+        got = kv.flatten(0, 1).double().cpu().numpy()
+        slots = want["slot_map"][:int(n2.sum())]
+        assert (np.abs(got[slots] - rows[:len(slots)]) <= 2.0 ** -8 * np.abs(rows[:len(slots)]) + 5e-5).all()
+        got[slots] = np.nan
+        assert np.isnan(got).all()
+
+
 def test_attention_far_offsets(cuda_ok):
     """Pages whose byte and element offsets pass 32 bits."""
     page, n_pages = 64, 62000                      # 62000 * 64 * 576 = 2.29e9 elements, 4.6 GB
