@@ -29,13 +29,13 @@
 // unit, which would bound the pair at 94% of the two SMs' peak.
 //
 // Measured (one B200, cold caches, merge included).  2048 tokens behind 16384 rows, 64
-// heads, bf16: 3.9 ms (1.27 PFLOP/s), 4.5 in a long run under the power limit; a unit
+// heads, bf16: 3.95 ms (1.26 PFLOP/s), 4.6 in a long run under the power limit; a unit
 // takes some 2900 cycles, and what exceeds 2304 is the keys' copies, which have one
 // tile's time to arrive from L2 in, and the MMA thread's waits.  Eight tokens at 32768
-// rows: 98 us (302 MB: 60 us of it at 5 TB/s, the rest the first tile's way through the
+// rows: 99 us (302 MB: 60 us of it at 5 TB/s, the rest the first tile's way through the
 // pipeline, the partials and their merge).  32 tokens at up to 24000 packed FP8 rows:
-// 182 us (215 MB): one S buffer, the widening, instruction fetch, and copies of
-// 656-byte rows, whose 128-byte pieces straddle lines.
+// 161 us (215 MB): with one S buffer the MMAs, the softmax and the widening, 3000 to
+// 4000 cycles a tile each, wait for one another.
 //
 // Split.  The units of the whole batch, in order, are cut into one equal range
 // per cluster, wherever the cuts fall: a batch of short and long sequences, or a
@@ -271,7 +271,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Two float32 operations in one instruction (a, b as pairs in one 64-bit register).
+// Two float32 operations in one instruction, on pairs in 64-bit registers (packed FP8
+// decode 169 us where single ones took 188: fewer instructions to fetch, no spills).
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
