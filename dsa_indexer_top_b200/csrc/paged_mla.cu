@@ -1175,15 +1175,20 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         if (!ok) break;
         // row statistics to the value CTA: both halves' sums joined, through the maxima's
         // place of the next tile's parity (a piece's result is out before the next
-        // piece's first P: see out_done)
+        // piece's first P: see out_done).  A row's sum goes in two halves to the places of
+        // its own two maxima: x_bar orders a quadrant's two warps and nothing else, so the
+        // exchange has to stay in the quadrant's own bytes.
         if (live) {
-            float *lx = reinterpret_cast<float *>(&sm->q.xmax[tile & 1][0][0]);
-            if (half == 1) lx[r] = l;
+            uint16_t(*lx)[kRows] = sm->q.xmax[tile & 1];
+            if (half == 1) {
+                lx[0][r] = static_cast<uint16_t>(__float_as_uint(l));
+                lx[1][r] = static_cast<uint16_t>(__float_as_uint(l) >> 16);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
             if (!wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
             xphase ^= 1;
-            if (half == 0) l += lx[r];
+            if (half == 0) l += u2f(static_cast<uint32_t>(lx[0][r]) | static_cast<uint32_t>(lx[1][r]) << 16);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->x_bar[quad]);  // read, before the place is written again
             if (!wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
