@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <climits>
+#include <utility>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -53,6 +54,10 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
     const dsa_verify &v = a.v;
     const int CL = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int r = blockIdx.x / CL, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // Shared memory of another CTA may be written once that CTA has begun: this arrival
+    // and the wait before the first such write say so (the pass over the row lies
+    // between the two, so the wait costs nothing).
+    auto begun = cluster.barrier_arrive();
     griddep_wait();
     const int D = v.n_draft, V = v.vocab;
     const T *pt = static_cast<const T *>(v.target) + r * v.t_req_stride;
@@ -132,7 +137,10 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
             s += __shfl_xor_sync(0xffffffffu, s, o);
             last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
         }
-        if (pass > 0) cluster.sync();  // every CTA has read the first pass's sums
+        if (pass == 0)
+            cluster.barrier_wait(std::move(begun));  // every CTA has begun
+        else
+            cluster.sync();  // every CTA has read the first pass's sums
         if (lane < CL) {
             *cluster.map_shared_rank(&seg[gw], lane) = s;
             *cluster.map_shared_rank(&last_s[gw], lane) = last;
