@@ -222,6 +222,10 @@ __device__ __forceinline__ void umma_e4m3_ta(uint32_t d_tmem, uint32_t a_tmem, u
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// For what ordinary reads and writes of this CTA precede.
+__device__ __forceinline__ void arrive_remote_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -1410,7 +1414,14 @@ __device__ void value_mma(const TcArgs &a, Small *sm, uint8_t *p_sm, uint8_t *v_
         }
         if (!ok) break;
         uint32_t good = 1;
-        if (lane == 0) good = post_command(a, sm, kCmdFinish, cphase, true) ? 1u : 0u;
+        if (lane == 0) {
+            good = post_command(a, sm, kCmdFinish, cphase, true) ? 1u : 0u;
+            // The output warps have arrived on cmd_done: their reads and writes of the P slots
+            // and of the row statistics, which the score CTA's copies overwrite next, come
+            // before this one arrival at cluster scope (their own would each wait for their
+            // stores to memory).
+            if (good) arrive_remote_release(map_rank(smem_u32(&sm->out_done), 0));
+        }
         good = __shfl_sync(0xffffffffu, good, 0);
         cphase = __shfl_sync(0xffffffffu, cphase, 0);
         if (!good) break;
@@ -1451,7 +1462,6 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
     const int r = 32 * quad + lane;
     const uint32_t tb = sm->tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + 256 * half;
-    const uint32_t r_done = map_rank(smem_u32(&sm->out_done), 0);
     uint32_t cphase = 0, piece = 0;
     Walk w(a, sm);
     Walk cw(a, sm);  // the units being widened
@@ -1589,8 +1599,6 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
                 const int end = static_cast<int>(((last + 1) * sm->plan_active - 1) / sm->plan_total);
                 a.meta[cluster] = Meta{end - cluster + 1, static_cast<int>(w.row0()), rows, 0};
             }
-            __syncwarp();
-            if (lane == 0) arrive_remote(r_done);
             ++piece;
             w.next();
         }
@@ -1643,7 +1651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&sm->p_got[i], 1);
             mbar_init(&sm->p_full[i], 8);
         }
-        mbar_init(&sm->out_done, 8);
+        mbar_init(&sm->out_done, 1);
         mbar_init(&sm->stat_full, 4);
         mbar_init(&sm->cmd_full, 2);
         mbar_init(&sm->cmd_done, 8);

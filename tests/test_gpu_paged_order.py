@@ -40,3 +40,18 @@ def test_many_short_pieces_under_load(cuda_ok, kind, heads):
         torch.cuda.synchronize()
         assert B.dsa_check_status(c.ws) == B.DSA_OK
         assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_results_are_out_before_the_next_piece(cuda_ok, kind):
+    """One-tile pieces: a result is staged where the next piece's weights arrive."""
+    c = Case([(i % 120, 1) for i in range(600)], heads=64, page=32, kind=kind, seed=32).run().check()
+    out, lse = c.out.clone(), c.lse.clone()
+    for _ in range(25):
+        c.out.fill_(77.0)
+        c.lse.fill_(77.0)
+        for _ in range(4):
+            B.dsa_paged_mla(c.batch, c.mla, c.ws)
+        torch.cuda.synchronize()
+        assert B.dsa_check_status(c.ws) == B.DSA_OK
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
