@@ -511,7 +511,9 @@ typedef struct {
  *   k_idx[seq][pos] = LayerNorm(y[576:704]) * ln_weight + ln_bias, its last 64
  *                     dims turned by RoPE(pos)
  *   ws   dsa_cache_writer_workspace_bytes(n_tok, hidden) bytes, 256-byte aligned
- *        (status word + split-K partials of y)
+ *        (status word + split-K partials of y): enough for either writer, this one
+ *        or dsa_write_paged_rows.  Each refuses only what is too small for its own
+ *        partials; this one's are fewer from 1024 tokens on.
  * Out-of-range tok_seq / tok_pos skip the token and set DSA_ERR_INVALID in the
  * workspace status word.
  */
