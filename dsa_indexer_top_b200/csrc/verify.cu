@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
     __shared__ double seg[kVerMaxCluster * kVerWarps];
     __shared__ int last_s[kVerMaxCluster * kVerWarps];
     __shared__ double run[kVerWarps];
-    __shared__ int acc_s, chosen_s;
+    __shared__ int acc_s, first_s, chosen_s;
     cg::cluster_group cluster = cg::this_cluster();
     const dsa_verify &v = a.v;
     const int CL = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
         acc = min(acc, n);
         if (lane == 0) acc_s = acc;
     }
-    if (tid == 0) chosen_s = -1;
+    if (tid == 0) chosen_s = -1, first_s = kVerThreads;
     __syncthreads();
     const int acc = acc_s;
     const bool rejected = acc < n;
@@ -177,14 +177,19 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
             const double y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
+        // a run starts at the very sum its predecessor ends with, so that no target falls
+        // between two runs
+        const double prev = __shfl_up_sync(0xffffffffu, inc, 1);
         if (lane == 31) run[warp] = inc;
         __syncthreads();
         for (int w = 0; w < warp; ++w) before += run[w];
-        const double start = before + (inc - c);
-        if (c > 0.0 && before + inc > target && !(start > target)) {
+        const unsigned past = __ballot_sync(0xffffffffu, c > 0.0 && before + inc > target);
+        if (lane == 0 && past) atomicMin(&first_s, 32 * warp + __ffs(past) - 1);
+        __syncthreads();
+        if (tid == first_s) {
             // this run crosses: its first entry past the target (its last with weight
             // where rounding leaves none)
-            double t = start;
+            double t = lane > 0 ? before + prev : before;
             int pick = -1;
             for (int j = a0; j < a1; ++j) {
                 const double w = weight(ld_p(prow, j), qr ? ld_p(qr, j) : 0.f, j);
@@ -194,12 +199,13 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
                     if (t > target) break;
                 }
             }
-            atomicMax(&chosen_s, pick);
+            chosen_s = pick;
+        } else if (tid == 0 && first_s == kVerThreads) {
+            // No run crosses: the segment's sum, added in another order than the runs',
+            // rounds past the target and theirs do not (its last entry with weight), or the
+            // target is at or past the total (u >= 1, rounding: the last of all).
+            chosen_s = last_s[sg] >= 0 ? last_s[sg] : any;
         }
-        __syncthreads();
-        // (no run crosses where the sums round past the total, or u >= 1: the last entry
-        // with weight)
-        if (tid == 0 && chosen_s < 0) chosen_s = any;
         __syncthreads();
         break;
     }
