@@ -92,10 +92,18 @@ static_assert(kQCol + 32 * kQTmem <= 512, "tensor memory");
 // and bf16, whose precision does not depend on the scale.
 constexpr float kRescale = 32.0f;
 // Packed FP8 rows: a weight times its row's scale goes to the MMA as fp16, 2^4 at the
-// reference maximum: below 2^15 (with a scale's mantissa) until that is raised, and
-// rounded to fp16's smallest step only 2^-28 under it.
+// reference maximum, which is of that product over the rows that a token sees: below
+// 2^15 (with a scale's mantissa) until the reference is raised, and rounded to fp16's
+// smallest step only 2^-28 under it.  Where the scales of a tile's rows lie within 2^8
+// of one another, the largest one stands for all of them, seen or not: the reference is
+// then up to 2^8 above the product, and the smallest step 2^-20 under it.
 constexpr float kRescaleFp8 = 10.0f;
 constexpr float kShiftFp8 = 4.0f;
+constexpr uint32_t kSpreadFp8 = 8u << 23;  // of a float's bits
+// A row's weight alone, in the same unit, is its product over its scale: scales below
+// 2^-60, or 2^-100 of the tile's largest, count as that much in the reference (log2),
+// which keeps the weights and their sum finite in float32.
+constexpr float kLowScaleFp8 = -60.0f, kLowInTileFp8 = -100.0f;
 constexpr uint32_t kNoRow = 0x80000000u;         // scale of a row nobody sees
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -128,7 +136,7 @@ struct Small {
     uint64_t fin;
     // packed FP8 rows
     uint64_t sig_full[2], sig_free[2];                // score CTA: row scales of the tiles of either parity
-    int sig_exp[2], sig_gap[2];                       // .. their power of two; some key of the tile has none
+    int sig_exp[2], sig_gap[2];                       // .. their power of two; 1: some key of the tile has none, 2: far apart
     uint64_t h_full[kHStages], h_free[kHStages];      // value CTA: widened units
     uint32_t tmem_base;
     int abort;
@@ -273,6 +281,18 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint32_
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 8 TMEM columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 // Two float32 operations in one instruction, on pairs in 64-bit registers (packed FP8
@@ -864,15 +884,19 @@ __device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
                         ++seen;
                     }
             }
-            float mx = 0.f;  // (of the finite ones: a token need not see the others)
+            // the largest of the finite ones (a token need not see the others), as bits
+            uint32_t mx = 0, mn = 0x7FFFFFFFu;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[i]) <= FLT_MAX ? fabsf(v[i]) : 0.f);
-            const bool gap = __any_sync(0xffffffffu, seen < 4);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t u = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+                mx = max(mx, u < 0x7F800000u ? u : 0u);
+                mn = i < seen ? min(mn, u) : mn;
+            }
+            mx = __reduce_max_sync(0xffffffffu, mx);
+            const bool spread = mn + kSpreadFp8 <= max(mx, kSpreadFp8);
+            const uint32_t flags = __reduce_or_sync(0xffffffffu, (seen < 4 ? 1u : 0u) | (spread ? 2u : 0u));
             // (2^-e multiplies a row's sum, which has to stay finite: no less than -80)
-            e = mx > 0.f ? min(max(e, -80), 120) : 0;
+            const int e = mx > 0 ? min(max(static_cast<int>(mx >> 23) - 127, -80), 120) : 0;
             const float down = u2f(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = i < seen ? v[i] * down + 0.f : -0.f;
@@ -881,7 +905,7 @@ __device__ void score_scales_fp8(const TcArgs &a, Small *sm) {
                 make_float4(v[0], v[1], v[2], v[3]);
             if (lane == 0) {
                 sm->sig_exp[tile & 1] = e;
-                sm->sig_gap[tile & 1] = gap;
+                sm->sig_gap[tile & 1] = static_cast<int>(flags);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->sig_full[tile & 1]);
@@ -975,6 +999,28 @@ __device__ __forceinline__ float bf16_up(float x) {
     return u2f((b & 0xFFFFu) && !(b >> 31) ? t + 0x10000u : t);
 }
 
+// Scales far apart: the maximum over 64 keys, those up to `last`, of the weight times its
+// own row's scale (log2).  The logits are read from tensor memory again, eight at a time
+// in a rolled loop: the scales of a sound cache hardly ever lie that far apart, and the
+// same unrolled in the loop over tiles took 173 us of decode where this takes 169.
+__device__ __forceinline__ float spread_max(uint32_t taddr, const float *sig, int last, float qs, float c2, float low) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 8) {
+        uint32_t x[8], y[8];
+        tmem_ld8(taddr + c, x);
+        tmem_ld8(taddr + kKeys + c, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float g = sig[c + i];
+            const float z = fmaf(u2f(x[i]) * g, qs, u2f(y[i]));
+            if (c + i <= last && __float_as_uint(g) != kNoRow) mx = fmaxf(mx, fmaf(z, c2, fmaxf(lg2(fabsf(g)), low)));
+        }
+    }
+    return mx;
+}
+
 template <bool kFp8>
 __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint32_t p_remote) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
@@ -998,8 +1044,15 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         for (int kt = w.k0; kt < w.k1; ++kt, ++tile) {
             const uint32_t slot = tile & 1;  // of P, and of bf16's S buffers
             const uint32_t sbuf = kFp8 ? 0 : slot;
-            if ((kFp8 && !wait_bar(&sm->sig_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) ||
-                !wait_bar(&sm->s_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
+            if (kFp8 && !wait_bar(&sm->sig_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
+                ok = false;
+                break;
+            }
+            // packed FP8 rows: the tile's row scales are 2^sig_exp times what is in sig (read
+            // before the wait for S: what comes after it is on the way to the next MMA)
+            const float te = kFp8 ? static_cast<float>(*reinterpret_cast<volatile int *>(&sm->sig_exp[slot])) : 0.f;
+            const int sgap = kFp8 ? *reinterpret_cast<volatile int *>(&sm->sig_gap[slot]) : 0;
+            if (!wait_bar(&sm->s_full[slot], (tile >> 1) & 1, a.p.status, &sm->abort)) {
                 ok = false;
                 break;
             }
@@ -1009,10 +1062,9 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             const float *sig = &sm->q.sigma[slot][64 * half];
             const uint32_t okbits =
                 kFp8 ? 0xFFu : *reinterpret_cast<volatile uint32_t *>(&sm->key_ok[slot]) >> (8 * half) & 0xFFu;
-            // packed FP8 rows: the tile's row scales are 2^sig_exp times what is in sig
-            const float te = kFp8 ? static_cast<float>(*reinterpret_cast<volatile int *>(&sm->sig_exp[slot])) : 0.f;
-            const bool gap = kFp8 ? *reinterpret_cast<volatile int *>(&sm->sig_gap[slot]) != 0 : okbits != 0xFFu;
+            const bool gap = kFp8 ? sgap != 0 : okbits != 0xFFu;
             uint32_t x[64];
+            float mspread = INFINITY;  // (scales far apart)
             if (used) {
                 if constexpr (!kFp8) {
                     tmem_ld32(tb + kKeys * slot, reinterpret_cast<uint32_t(&)[32]>(x[0]));
@@ -1044,39 +1096,46 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->s_free[sbuf]);
+            auto free_s = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->s_free[sbuf]);
+            };
+            if (!kFp8) free_s();
             float mx = -INFINITY;
             // some logit is not finite, in a tile of tokens that do not see the same rows: the
             // row's values may be NaN, and 0 x NaN is NaN for those that do not see it (see
             // clean_stage)
             bool nf = false;
             const int s0 = kt * kKeys + 64 * half;
-            if (used) {
-                if (s0 + 63 > pos0 || gap) {
-                    float z4[4] = {0.f, 0.f, 0.f, 0.f};  // NaN where a logit is not finite
-                    if (kFp8 && pos0 < w.s.len - 1) {    // (in the loop below it would spill)
+            if (used && (s0 + 63 > pos0 || gap)) {
+                if (kFp8 && (sgap & 2))  // (reads S, so S is free only behind it)
+                    mspread = spread_max(tb, sig, pos - s0, q8s * ex2(te), c2,
+                                         fmaxf(kLowInTileFp8, kLowScaleFp8 - te)) + te;
+                float z4[4] = {0.f, 0.f, 0.f, 0.f};  // NaN where a logit is not finite
+                if (kFp8 && pos0 < w.s.len - 1) {    // (in the loop below it would spill)
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) z4[i & 3] = fmaf(u2f(x[i]), 0.f, z4[i & 3]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        if (!kFp8) z4[i & 3] = fmaf(u2f(x[i]), 0.f, z4[i & 3]);
-                        if (s0 + i > pos || (kFp8 ? __float_as_uint(sig[i]) == kNoRow : !((okbits >> (i / 8)) & 1)))
-                            x[i] = 0xFF800000u;
-                    }
-                    nf = __any_sync(0xffffffffu, r < rows && pos0 < w.s.len - 1 && !((z4[0] + z4[1]) + (z4[2] + z4[3]) == 0.f));
+                    for (int i = 0; i < 64; ++i) z4[i & 3] = fmaf(u2f(x[i]), 0.f, z4[i & 3]);
                 }
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    if (!kFp8) z4[i & 3] = fmaf(u2f(x[i]), 0.f, z4[i & 3]);
+                    if (s0 + i > pos || (kFp8 ? __float_as_uint(sig[i]) == kNoRow : !((okbits >> (i / 8)) & 1)))
+                        x[i] = 0xFF800000u;
+                }
+                nf = __any_sync(0xffffffffu, r < rows && pos0 < w.s.len - 1 && !((z4[0] + z4[1]) + (z4[2] + z4[3]) == 0.f));
+            }
+            if (kFp8) free_s();
+            if (used) {
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int i = 0; i < 64; i += 4)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], u2f(x[i + k]));
-                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                // (the running maximum is of the weight times the tile's power of two, which
-                // bounds what the MMA gets)
-                mx = bf16_up(fmaf(mx, c2, te));  // (scale > 0)
+                // (scale > 0; packed FP8 rows: the weight times the tile's power of two)
+                mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), c2, te);
+                if (kFp8) mx = fminf(mx, mspread);
+                mx = bf16_up(mx);
             }
             float al = 1.f;
             if (live) {

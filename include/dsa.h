@@ -675,6 +675,10 @@ typedef struct {
  * Device-detected errors set DSA_ERR_INVALID in the status word: a sequence whose
  * q_begin or seq_len is out of range is skipped, a page outside the pool counts
  * as rows nobody sees.
+ * Packed FP8 rows may have scales of any size next to one another: on the tensor
+ * cores a row's softmax weight times its scale enters the sum with 11 bits, and with
+ * an error of up to 2^-20 of the largest such product among the rows a token sees
+ * (scales below 2^-60 count as 2^-60 there).
  * Paths: bf16 queries with up to 128 heads x (512 + 64) over bf16 or packed FP8
  * rows run on tcgen05 tensor cores when page_rows is a multiple of 8, the scale is
  * positive and q, out, kv and the pool's strides are multiples of 16 bytes; other
