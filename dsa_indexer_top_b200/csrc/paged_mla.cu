@@ -1787,7 +1787,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // The latent part of each query row (token, head) as s (q1 + q2): s a power of two
 // that brings the row's largest value under E4M3's 448, q1 the nearest E4M3 value, q2
-// the nearest to what is left (exact but below 2^-18 of the row's largest value).
+// the nearest to what is left (exact but below 2^-18 of the row's largest value).  A
+// row with an infinity gets NaN for s: as codes it would be finite, and its logits with it.
 // One warp per row, 16 dims per lane; bound by launch latency at decode sizes.
 __global__ void __launch_bounds__(256) split_queries_kernel(const __nv_bfloat16 *q, uint8_t *q8, float *scale, int64_t rows) {
     griddep_wait();
@@ -1830,7 +1831,7 @@ __global__ void __launch_bounds__(256) split_queries_kernel(const __nv_bfloat16 
     uint4 *dst = reinterpret_cast<uint4 *>(q8 + row * 2 * kLatent + 16 * lane);
     dst[0] = make_uint4(t1[0], t1[1], t1[2], t1[3]);
     dst[kLatent / 16] = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-    if (lane == 0) scale[row] = u2f(static_cast<uint32_t>(127 + k) << 23);
+    if (lane == 0) scale[row] = u2f(mx <= FLT_MAX ? static_cast<uint32_t>(127 + k) << 23 : 0x7FC00000u);
 }
 
 // Merge of the row tiles that a cut divided: o = sum_i 2^(m_i - M) o_i / sum_i
