@@ -156,7 +156,7 @@ struct Small {
         } q;
         struct {
             float alpha[2][kRows];  // value CTA: [slot][row]
-            float m[kRows], l[kRows];
+            float factor[kRows];    // .. what a piece's O is multiplied by
         } v;
     };
 };
@@ -1022,14 +1022,14 @@ __device__ __forceinline__ float spread_max(uint32_t taddr, const float *sig, in
 }
 
 template <bool kFp8>
-__device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint32_t p_remote) {
+__device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint32_t p_remote, int cluster) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
     const int r = 32 * quad + lane;
     const uint32_t tb = (static_cast<uint32_t>(32 * quad) << 16) + 64 * half;
     const float c2 = a.p.scale * kLog2e;
     const uint32_t r_alpha = map_rank(smem_u32(&sm->v.alpha[0][0]), 1), r_flags = map_rank(smem_u32(&sm->flags[0][0]), 1);
     const uint32_t r_pfull = map_rank(smem_u32(&sm->p_full[0]), 1), r_stat = map_rank(smem_u32(&sm->stat_full), 1);
-    const uint32_t r_m = map_rank(smem_u32(&sm->v.m[0]), 1), r_l = map_rank(smem_u32(&sm->v.l[0]), 1);
+    const uint32_t r_factor = map_rank(smem_u32(&sm->v.factor[0]), 1);
     uint32_t tile = 0, piece = 0, xphase = 0;
     bool ok = true;
     for (Walk w(a, sm); ok && w.valid(); w.next(), ++piece) {
@@ -1040,7 +1040,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         const int pos = w.s.len - w.s.n + tok;
         const int pos0 = w.s.len - w.s.n + w.rt * a.tok_tile;  // the tile's first token
         const float q8s = kFp8 ? a.q8_scale[w.row0() + min(r, rows - 1)] : 0.f;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, lp = 0.f;  // lp: of the rounded weights
         for (int kt = w.k0; kt < w.k1; ++kt, ++tile) {
             const uint32_t slot = tile & 1;  // of P, and of bf16's S buffers
             const uint32_t sbuf = kFp8 ? 0 : slot;
@@ -1156,6 +1156,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                     al = ex2(m - mx);
                     m = mx;
                     l *= al;
+                    lp *= al;
                 }
             }
             const bool flag = __any_sync(0xffffffffu, al != 1.f);
@@ -1167,7 +1168,7 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
             if (used) {
                 const float mu = (m == -INFINITY ? 0.f : m) - (kFp8 ? kShiftFp8 + te : 0.f);
                 const uint64_t c22 = pair(c2, c2), mu2 = pair(-mu, -mu);
-                uint64_t l2[2] = {0, 0};
+                uint64_t l2[2] = {0, 0}, lp2[2] = {0, 0};
                 uint8_t *pl = p_stage + slot * kPSlot + half * 2 * kBlk;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -1190,14 +1191,23 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
                             p[2 * i + 1] = z.y;
                         }
                     }
-                    // bf16 (fp16) weights for the MMA; the sum keeps the float32 values, so the
-                    // roundings (half a step, 2^-8 relative) average out in the output
-                    *reinterpret_cast<uint4 *>(pl + sw128_offset(r, c)) =
-                        kFp8 ? make_uint4(pack_f16(p[0], p[1]), pack_f16(p[2], p[3]), pack_f16(p[4], p[5]),
-                                          pack_f16(p[6], p[7]))
-                             : make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
-                                          pack_bf16(p[6], p[7]));
+                    // bf16 (fp16) weights for the MMA, off by at most half a step, 2^-8 (2^-11) of a
+                    // weight.  bf16: O is divided by the sum of the rounded weights, so that an
+                    // error that few rows with all the weight share cancels (one such row is
+                    // returned as it is); error of the output 0.0017 (float32 weights 0.00165)
+                    // where the sum of the float32 weights gave 0.0023, for 2 to 3% of the time.
+                    // That sum is for the lse.
+                    uint4 pk;
+                    uint32_t *pw = reinterpret_cast<uint32_t *>(&pk);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        pw[i] = kFp8 ? pack_f16(p[2 * i], p[2 * i + 1]) : pack_bf16(p[2 * i], p[2 * i + 1]);
+                        if (!kFp8) lp2[i & 1] = add2(lp2[i & 1], pair(u2f(pw[i] << 16), u2f(pw[i] & 0xFFFF0000u)));
+                    }
+                    *reinterpret_cast<uint4 *>(pl + sw128_offset(r, c)) = pk;
                 }
+                const float2 lps = unpair(add2(lp2[0], lp2[1]));
+                if (!kFp8) lp += lps.x + lps.y;
                 const float2 ls = unpair(add2(l2[0], l2[1]));
                 const float lt = ls.x + ls.y;
                 l += kFp8 ? lt * ex2(-te) : lt;
@@ -1243,28 +1253,47 @@ __device__ void score_softmax(const TcArgs &a, Small *sm, uint8_t *p_stage, uint
         // exchange has to stay in the quadrant's own bytes.
         if (live) {
             uint16_t(*lx)[kRows] = sm->q.xmax[tile & 1];
-            if (half == 1) {
-                lx[0][r] = static_cast<uint16_t>(__float_as_uint(l));
-                lx[1][r] = static_cast<uint16_t>(__float_as_uint(l) >> 16);
+#pragma unroll 1
+            for (int i = 0; i < (kFp8 ? 1 : 2); ++i) {
+                const float sum = i == 0 ? l : lp;
+                if (half == 1) {
+                    lx[0][r] = static_cast<uint16_t>(__float_as_uint(sum));
+                    lx[1][r] = static_cast<uint16_t>(__float_as_uint(sum) >> 16);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
+                ok = ok && wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort);
+                xphase ^= 1;
+                const float other = u2f(static_cast<uint32_t>(lx[0][r]) | static_cast<uint32_t>(lx[1][r]) << 16);
+                if (half == 0 && i == 0) l += other;
+                if (half == 0 && i == 1) lp += other;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->x_bar[quad]);  // read, before the place is written again
+                ok = ok && wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort);
+                xphase ^= 1;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->x_bar[quad]);
-            if (!wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
-            xphase ^= 1;
-            if (half == 0) l += u2f(static_cast<uint32_t>(lx[0][r]) | static_cast<uint32_t>(lx[1][r]) << 16);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->x_bar[quad]);  // read, before the place is written again
-            if (!wait_bar(&sm->x_bar[quad], xphase, a.p.status, &sm->abort)) break;
-            xphase ^= 1;
+            if (!ok) break;
         }
         if (half == 0) {
             if (piece > 0 && !wait_bar(&sm->out_done, (piece - 1) & 1, a.p.status, &sm->abort)) break;
             if (live) {
-                st_remote(r_m + r * 4, __float_as_uint(kFp8 ? m - kShiftFp8 : m), r_stat);
-                st_remote(r_l + r * 4, __float_as_uint(l), r_stat);
+                // a whole piece is divided by its sum and done; a partial one keeps l as its sum
+                const bool whole = w.k0 == 0 && w.k1 == w.nk;
+                const float d = kFp8 ? l : lp, mr = kFp8 ? m - kShiftFp8 : m;
+                const float factor = d != 0.f ? (whole ? 1.f : l) / d : 0.f;
+                if (r < rows) {
+                    const int64_t pslot = 2 * cluster + (w.k0 == 0 ? 1 : 0);
+                    if (!whole) {
+                        a.part_ml[pslot * 2 * kRows + r] = mr;
+                        a.part_ml[(pslot * 2 + 1) * kRows + r] = l;
+                    } else if (a.p.lse) {
+                        a.p.lse[w.row0() + r] = l != 0.f ? mr * kLn2 + logf(l) : -INFINITY;
+                    }
+                }
+                st_remote(r_factor + r * 4, __float_as_uint(factor), r_stat);
             }
             __syncwarp();
-            if (lane == 0) arrive_expect_remote(r_stat, live ? 256 : 0);
+            if (lane == 0) arrive_expect_remote(r_stat, live ? 128 : 0);
         }
     }
 }
@@ -1599,9 +1628,7 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
         } else {
             if (!wait_bar(&sm->stat_full, piece & 1, a.p.status, &sm->abort)) break;
             const int rows = w.rows();
-            const bool live = r < rows;
-            const float l = sm->v.l[r], m = sm->v.m[r];
-            const float inv = l != 0.f ? 1.f / l : 0.f;
+            const float factor = sm->v.factor[r];
             const bool whole = w.k0 == 0 && w.k1 == w.nk;
             const int64_t row = w.row0() + r;
             const int64_t pslot = 2 * cluster + (w.k0 == 0 ? 1 : 0);
@@ -1622,10 +1649,10 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             *reinterpret_cast<uint4 *>(st + lane * 256 + (((4 * g + i / 8) ^ (lane & 15)) << 4)) =
-                                make_uint4(pack_bf16(u2f(x[i]) * inv, u2f(x[i + 1]) * inv),
-                                           pack_bf16(u2f(x[i + 2]) * inv, u2f(x[i + 3]) * inv),
-                                           pack_bf16(u2f(x[i + 4]) * inv, u2f(x[i + 5]) * inv),
-                                           pack_bf16(u2f(x[i + 6]) * inv, u2f(x[i + 7]) * inv));
+                                make_uint4(pack_bf16(u2f(x[i]) * factor, u2f(x[i + 1]) * factor),
+                                           pack_bf16(u2f(x[i + 2]) * factor, u2f(x[i + 3]) * factor),
+                                           pack_bf16(u2f(x[i + 4]) * factor, u2f(x[i + 5]) * factor),
+                                           pack_bf16(u2f(x[i + 6]) * factor, u2f(x[i + 7]) * factor));
                     }
                     if (c == 128) fence_proxy_async_smem();  // (the slots are next written by a copy)
                     __syncwarp();
@@ -1641,15 +1668,7 @@ __device__ void value_output(const TcArgs &a, Small *sm, uint8_t *stage, const u
                     tmem_ld32(tb + c, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) po[(c + i) * kRows] = u2f(x[i]);
-                }
-            }
-            if (live && half == 0) {
-                if (!whole) {
-                    a.part_ml[pslot * 2 * kRows + r] = m;
-                    a.part_ml[(pslot * 2 + 1) * kRows + r] = l;
-                } else if (a.p.lse) {
-                    a.p.lse[row] = l != 0.f ? m * kLn2 + logf(l) : -INFINITY;
+                    for (int i = 0; i < 32; ++i) po[(c + i) * kRows] = u2f(x[i]) * factor;
                 }
             }
             if (tid == 0 && w.k0 == 0 && w.k1 < w.nk) {
@@ -1751,7 +1770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0) {
         uint8_t *stage = smem + kQBytes, *ring = stage + 2 * kPSlot;
         if (warp < 8) {
-            score_softmax<kFp8>(a, sm, stage, map_rank(smem_u32(smem), 1));
+            score_softmax<kFp8>(a, sm, stage, map_rank(smem_u32(smem), 1), cluster);
         } else if (kFp8) {
             if (warp == 8)
                 score_producer_fp8(a, sm, smem, stage, ring, ring + 2 * kCodes, &maps.q, &maps.q8, &maps.k, &maps.r);
