@@ -195,6 +195,14 @@ class _CStruct:
             object.__setattr__(self, "_cs", cs)
         return cs
 
+    def checked(self, check, other=None):
+        """The value of check(self, other), found once and kept until a field of either is assigned."""
+        was = self.__dict__.get("_ok")
+        if was is None or was[0] is not self.c() or (other is not None and was[1] is not other.c()):
+            was = (self.c(), other and other.c(), check(self) if other is None else check(self, other))
+            object.__setattr__(self, "_ok", was)
+        return was[2]
+
 
 @dataclass
 class Queries(_CStruct):
@@ -288,9 +296,39 @@ def _rows_int32(table: torch.Tensor):
         raise TypeError("the block table is int32 [n_seq, max_pages] with contiguous rows")
 
 
+def _device_of(*tensors) -> int:
+    """The one device that holds the tensors (pinned host memory may stand beside it)."""
+    dev = -1
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d == dev >= 0 or t.numel() == 0:
+            continue
+        if d < 0 and not (torch.cuda.is_available() and t.is_pinned()):
+            raise ValueError("expected tensors on the GPU")
+        if d >= 0 and dev >= 0:
+            raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
+        dev = max(dev, d)
+    return dev
+
+
+def _stream_on(dev: int, ws: torch.Tensor, stream):
+    """The launch's stream; the kernels run on the current device, which has to hold the tensors."""
+    at = ws.get_device()
+    if at < 0:
+        raise ValueError("expected tensors on the GPU")
+    here = torch.cuda.current_device()
+    if at != here or (dev != here and dev >= 0):
+        raise ValueError(f"tensors on cuda:{dev}, the workspace on cuda:{at}, the current device is cuda:{here}")
+    if stream is None and _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(here))
+    return _stream(stream)
+
+
 def _dp(t: Optional[torch.Tensor]):
-    """Address of a tensor's first element, None for an empty tensor or none."""
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    """Address of a tensor's first element; no address for an empty tensor or none."""
+    return None if t is None else t.data_ptr()
 
 
 @dataclass
@@ -514,31 +552,63 @@ def dsa_up_project(o_lat: torch.Tensor, w_uv: torch.Tensor, out: torch.Tensor, w
                                 ws.numel() * ws.element_size(), _stream(stream)), "dsa_up_project")
 
 
+def _plan_device(plan: PagePlan) -> int:
+    return _device_of(plan.ctx_len, plan.new_len, plan.held, plan.free_pages, plan.free_begin, plan.block_table,
+                      plan.q_begin, plan.seq_len, plan.q_seq, plan.q_pos, plan.slot_map, plan.held_out, plan.free_used)
+
+
 def dsa_page_tables(plan: PagePlan, ws: torch.Tensor, stream=None):
-    pc = plan.c()
-    _check(lib().dsa_page_tables(ctypes.byref(pc), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "dsa_page_tables")
+    dev, pc = plan.checked(_plan_device), plan.c()
+    _check(lib().dsa_page_tables(ctypes.byref(pc), _ptr(ws), ws.nbytes, _stream_on(dev, ws, stream)), "dsa_page_tables")
+
+
+def _paged_writer(writer: CacheWriter) -> int:
+    n, hidden = writer.h.shape
+    if writer.kv is not None and writer.k_idx is not None and writer.kv.shape[:2] != writer.k_idx.shape[:2]:
+        raise ValueError("kv and k_idx hold the same pages and rows")
+    _int32(writer.tok_pos)
+    if writer.tok_pos.numel() != n:
+        raise ValueError("tok_pos holds one position per token")
+    for t, dtype, size in ((writer.h, torch.bfloat16, 0), (writer.w, torch.bfloat16, 704 * hidden),
+                           (writer.kv, torch.bfloat16, 0), (writer.k_idx, torch.bfloat16, 0),
+                           (writer.rms_weight, torch.float32, 512), (writer.ln_weight, torch.float32, 128),
+                           (writer.ln_bias, torch.float32, 128)):
+        if t is not None and (t.dtype != dtype or t.numel() < size or (size and not t.is_contiguous())
+                              or (t.dim() > 1 and t.numel() and t.stride(-1) != 1)):
+            raise TypeError(f"expected {dtype} with contiguous rows, got {t.dtype} {tuple(t.shape)}")
+    for t, width in ((writer.kv, 576), (writer.k_idx, 128)):
+        if t is not None and (t.dim() != 3 or t.shape[2] < width):
+            raise ValueError("the pools are [n_pages, page_rows, row], rows of 576 and 128")
+    return _device_of(writer.h, writer.w, writer.rms_weight, writer.ln_weight, writer.ln_bias, writer.tok_pos, writer.kv,
+                      writer.k_idx)
 
 
 def dsa_write_paged_rows(writer: CacheWriter, slot_map: torch.Tensor, ws: torch.Tensor, stream=None):
     """writer.kv [n_pages, page_rows, 576] and writer.k_idx [n_pages, page_rows, 128]; slot_map int32 [n_tok]."""
     _int32(slot_map)
-    wc = writer.c()
+    dev, wc = writer.checked(_paged_writer), writer.c()
     if slot_map.numel() != wc.n_tok:
         raise ValueError("slot_map holds one slot per token")
-    if writer.kv is not None and writer.k_idx is not None and writer.kv.shape[:2] != writer.k_idx.shape[:2]:
-        raise ValueError("kv and k_idx hold the same pages and rows")
-    _check(lib().dsa_write_paged_rows(ctypes.byref(wc), _ptr(slot_map), _ptr(ws), ws.numel() * ws.element_size(),
-                                      _stream(stream)), "dsa_write_paged_rows")
+    if slot_map.get_device() != dev and wc.n_tok:
+        dev = _device_of(writer.h, slot_map)
+    _check(lib().dsa_write_paged_rows(ctypes.byref(wc), _ptr(slot_map), _ptr(ws), ws.nbytes, _stream_on(dev, ws, stream)),
+           "dsa_write_paged_rows")
 
 
-def _paged_shapes(batch: PagedBatch, mla: Mla):
-    kv = mla.kv
+def _paged_shapes(batch: PagedBatch, mla: Mla) -> int:
+    kv, q, out, lse, n = mla.kv, mla.q, mla.out, mla.lse, batch.n_tok
     if kv.dim() != 3 or kv.shape[0] < batch.n_pages or kv.shape[1] < batch.page_rows:
         raise ValueError("the pool is [n_pages, page_rows, row]")
-    if mla.q.shape[0] < batch.n_tok or mla.out.shape[0] < batch.n_tok or (mla.lse is not None and
-                                                                           mla.lse.shape[0] < batch.n_tok):
+    if q.shape[0] < n or out.shape[0] < n or (lse is not None and lse.shape[0] < n):
         raise ValueError("queries and outputs hold n_tok rows")
+    if kv.dtype not in (q.dtype, torch.uint8) or out.dtype != q.dtype or (lse is not None and lse.dtype != torch.float32):
+        raise TypeError("queries, outputs and the pool are of one type (a uint8 pool: packed FP8 rows), the lse float32")
+    if not (q.is_contiguous() and out.is_contiguous() and (lse is None or lse.is_contiguous())) or kv.stride(2) != 1:
+        raise TypeError("queries, outputs, the lse and the pool's rows are contiguous")
+    if (kv.shape[2] < (DSA_MLA_FP8_ROW_BYTES if kv.dtype == torch.uint8 else q.shape[2]) or mla.d_latent > q.shape[2]
+            or out.numel() < n * q.shape[1] * mla.d_latent or (lse is not None and lse.numel() < n * q.shape[1])):
+        raise ValueError("pool rows, outputs or the lse are too small for the queries")
+    return _device_of(batch.block_table, batch.q_begin, batch.seq_len, q, kv, out, lse)
 
 
 def dsa_paged_mla_workspace_bytes(batch: PagedBatch, mla: Mla) -> int:
@@ -546,10 +616,9 @@ def dsa_paged_mla_workspace_bytes(batch: PagedBatch, mla: Mla) -> int:
 
 
 def dsa_paged_mla(batch: PagedBatch, mla: Mla, ws: torch.Tensor, stream=None):
-    _paged_shapes(batch, mla)
-    bc, mc = batch.c(), mla.c()
-    _check(lib().dsa_paged_mla(ctypes.byref(bc), ctypes.byref(mc), _ptr(ws), ws.numel() * ws.element_size(),
-                               _stream(stream)), "dsa_paged_mla")
+    dev, bc, mc = batch.checked(_paged_shapes, mla), batch.c(), mla.c()
+    _check(lib().dsa_paged_mla(ctypes.byref(bc), ctypes.byref(mc), _ptr(ws), ws.nbytes, _stream_on(dev, ws, stream)),
+           "dsa_paged_mla")
 
 
 def dsa_verify_drafts(target: torch.Tensor, draft_tokens: torch.Tensor, accept_u: torch.Tensor,
@@ -563,18 +632,17 @@ def dsa_verify_drafts(target: torch.Tensor, draft_tokens: torch.Tensor, accept_u
     _int32(draft_tokens, tokens, n_accept, n_draft)
     if any(u.dtype != torch.float32 or not u.is_contiguous() for u in (accept_u, sample_u)):
         raise TypeError("accept_u and sample_u are contiguous float32")
-    if (tuple(draft_tokens.shape) != (n, d) or tuple(accept_u.shape) != (n, d) or tuple(tokens.shape) != (n, d + 1)
+    if (draft_tokens.shape != (n, d) or accept_u.shape != (n, d) or tokens.shape != (n, d + 1)
             or sample_u.numel() != n or n_accept.numel() != n or (n_draft is not None and n_draft.numel() != n)
-            or (draft is not None and tuple(draft.shape) != (n, d, v))):
+            or (draft is not None and draft.shape != (n, d, v))):
         raise ValueError("verify: tensors of different shapes")
-    if (v > 1 and target.stride(2) != 1) or (draft is not None and (draft.dtype != target.dtype or
-                                                                     (v > 1 and draft.numel() and draft.stride(2) != 1))):
+    ts, ds = target.stride(), (0, 0, 1) if draft is None else draft.stride()
+    if (v > 1 and (ts[2] != 1 or (ds[2] != 1 and draft.numel()))) or (draft is not None and draft.dtype != target.dtype):
         raise TypeError("probability rows are contiguous and of one type")
-    vc = _Verify(n, d, v, _dtype_code(target), _dp(target), target.stride(0), target.stride(1), _dp(draft),
-                 0 if draft is None else draft.stride(0), 0 if draft is None else draft.stride(1), _dp(draft_tokens),
+    dev = _device_of(target, draft, draft_tokens, n_draft, accept_u, sample_u, tokens, n_accept)
+    vc = _Verify(n, d, v, _dtype_code(target), _dp(target), ts[0], ts[1], _dp(draft), ds[0], ds[1], _dp(draft_tokens),
                  _dp(n_draft), _dp(accept_u), _dp(sample_u), _dp(tokens), _dp(n_accept))
-    _check(lib().dsa_verify_drafts(ctypes.byref(vc), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "dsa_verify_drafts")
+    _check(lib().dsa_verify_drafts(ctypes.byref(vc), _ptr(ws), ws.nbytes, _stream_on(dev, ws, stream)), "dsa_verify_drafts")
 
 
 # ------------------------------------------------------------------ conveniences
