@@ -2,6 +2,7 @@
 // the kernels (indexer.cu, topk.cu, mla.cu).  Not part of the public header.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <map>
@@ -50,12 +51,16 @@ cudaError_t set_max_dynamic_smem(void (*kernel)(KArgs...), int bytes) {
     return e;
 }
 
-// SMs of the current device.
-inline int sm_count_current() {
+// SMs of the current device (asked once per device).
+inline int sm_count() {
+    static std::atomic<int> cache[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-        return 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
     return n;
 }
 

@@ -407,14 +407,13 @@ dsa_status dsa_page_tables(const dsa_page_plan *p, void *ws, size_t ws_bytes, vo
     PageTablesArgs a;
     a.p = *p;
     a.status = static_cast<uint32_t *>(ws);
-    return launch_page_tables(a, sm_count_current(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? DSA_OK
-                                                                                                      : DSA_ERR_CUDA;
+    return launch_page_tables(a, sm_count(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 size_t dsa_paged_mla_workspace_bytes(const dsa_paged_batch *batch, const dsa_mla *mla) {
     if (check_batch(batch) != DSA_OK || check_mla_layers(mla, 1) != DSA_OK) return 0;
     const PagedMlaArgs a = paged_args(batch, mla, nullptr);
-    return kStatus + (paged_mla_tc_shape(a) ? paged_mla_tc_scratch(a, sm_count_current()) : 0);
+    return kStatus + (paged_mla_tc_shape(a) ? paged_mla_tc_scratch(a, sm_count()) : 0);
 }
 
 dsa_status dsa_paged_mla(const dsa_paged_batch *batch, const dsa_mla *mla, void *ws, size_t ws_bytes, void *stream) {
@@ -432,9 +431,9 @@ dsa_status dsa_paged_mla(const dsa_paged_batch *batch, const dsa_mla *mla, void 
     if (mla->heads > 65535 || mla->d_latent + mla->d_rope > kGenMaxDims) return DSA_ERR_UNSUPPORTED;
     const PagedMlaArgs a = paged_args(batch, mla, ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = paged_mla_tc_shape(a) ? launch_paged_mla_tc(a, static_cast<uint8_t *>(ws) + kStatus,
-                                                                      sm_count_current(), st)
-                                                : launch_paged_mla_generic(a, st);
+    const cudaError_t e = paged_mla_tc_shape(a)
+                              ? launch_paged_mla_tc(a, static_cast<uint8_t *>(ws) + kStatus, sm_count(), st)
+                              : launch_paged_mla_generic(a, st);
     return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

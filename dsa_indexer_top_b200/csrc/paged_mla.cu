@@ -357,8 +357,9 @@ __device__ __forceinline__ int tile_keys(const Seq &s, int tt, int rt) {
     return (tile_seen(s, tt, rt) + kKeys - 1) / kKeys;
 }
 
-// sum_{i < n} floor((a i + b) / 128), in O(log 128) steps (a <= 128, n < 2^24: a n
-// stays in 32 bits).
+// sum_{i < n} floor((a i + b) / 128): points under a line, by the Euclidean reduction that
+// swaps its axes (slope and divisor as in a gcd), in O(log 128) steps (a <= 128, n < 2^24:
+// a n stays in 32 bits).
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t a, uint32_t b) {
     long long r = static_cast<long long>(n) * (b >> 7);
     b &= 127;
@@ -1393,7 +1394,8 @@ __device__ __forceinline__ bool post_command(const TcArgs &a, Small *sm, int cmd
 
 // A stage's values that are not finite (an exponent of all ones) become zeros.  For
 // the tiles in which some token does not see such a row: the tokens that do see it
-// have NaN weights there, from a logit that is NaN or infinite as well.  One warp, some
+// have NaN weights there, from a logit that is NaN or +infinity as well (with -infinity
+// the row has no weight and, cleaned, adds nothing).  One warp, some
 // 5 us a tile: the rows of a sound cache never come here.
 __device__ __forceinline__ void clean_stage(uint8_t *v, int lane, uint32_t expo) {
 #pragma unroll 1

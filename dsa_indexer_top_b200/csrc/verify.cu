@@ -278,7 +278,7 @@ extern "C" dsa_status dsa_verify_drafts(const dsa_verify *v, void *ws, size_t ws
     dsa::VerifyArgs a;
     a.v = *v;
     a.status = static_cast<uint32_t *>(ws);
-    return dsa::launch_verify(a, dsa::sm_count_current(), static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return dsa::launch_verify(a, dsa::sm_count(), static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? DSA_OK
                : DSA_ERR_CUDA;
 }
