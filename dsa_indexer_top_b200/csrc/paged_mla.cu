@@ -28,14 +28,16 @@
 // Both products have full-rate shapes: 36 x 64 cycles for S and 16 x 128 for O per
 // unit, which would bound the pair at 94% of the two SMs' peak.
 //
-// Measured (one B200, cold caches, merge included).  2048 tokens behind 16384 rows, 64
-// heads, bf16: 3.95 ms (1.26 PFLOP/s), 4.6 in a long run under the power limit; a unit
-// takes some 2900 cycles, and what exceeds 2304 is the keys' copies, which have one
-// tile's time to arrive from L2 in, and the MMA thread's waits.  Eight tokens at 32768
-// rows: 99 us (302 MB: 60 us of it at 5 TB/s, the rest the first tile's way through the
-// pipeline, the partials and their merge).  32 tokens at up to 24000 packed FP8 rows:
-// 161 us (215 MB): with one S buffer the MMAs, the softmax and the widening, 3000 to
-// 4000 cycles a tile each, wait for one another.
+// Measured (one B200, calls back to back over inputs that are not in the caches, all
+// launches included).  2048 tokens behind 16384 rows, 64 heads, bf16: 4.5 ms (1.1
+// PFLOP/s; the power limit lowers the clock, single calls with pauses take 4.05); a unit
+// takes some 3000 cycles, and what exceeds 2304 is the keys' copies, which have one
+// tile's time to arrive from L2 in, and the MMA thread's waits.  One token at 777 rows:
+// 22 us, the fixed part of every call: plan, query, the first tile's way through the
+// pipeline, partials and their merge.  Eight tokens at 32768 rows: 99 us, 303 MB at 4
+// TB/s behind that part.  32 tokens at up to 24000 packed FP8 rows: 163 us (215 MB): with
+// one S buffer the MMAs, the softmax and the widening, 3000 to 4000 cycles a tile each,
+// wait for one another.
 //
 // Split.  The units of the whole batch, in order, are cut into one equal range
 // per cluster, wherever the cuts fall: a batch of short and long sequences, or a

@@ -216,10 +216,11 @@ void cache_plan(int n_tok, int hidden, int bn, int &m_tiles, int &k_splits, int 
 
 // The paged writer's contraction.  Tiles of 256 output columns from 1024 tokens on
 // (the operands' way from L2 bounds the GEMM, and wider tiles read the hidden states
-// half as often: 2048 tokens 31.7 us against 46.6, 1024 23.2 against 24.2, but 512
-// 20.5 against 17.3); CUDA cores up to 4 tokens (11.5 us; 13 tokens 26.2 us against
-// 10.6 on the tensor cores).  The contiguous writer keeps its plan, and with it the
-// order of its sums.
+// half as often: 2048 tokens 37.0 us against 52.4, 1024 26.4 against 26.1, 512 22.5
+// against 19.3); CUDA cores up to 4 tokens (1 token 8.7 us against 10.6 on the tensor
+// cores, 4 tokens 11.0 against 10.2, 5 tokens 15.7 against 10.3, 13 tokens 25.8 against
+// 10.1).  (hidden 6144, both launches, back to back over five sets of inputs.)  The
+// contiguous writer keeps its plan, and with it the order of its sums.
 int paged_bn(int n_tok) { return n_tok >= 1024 ? 256 : 128; }
 constexpr int kPagedSkinnyMax = 4;
 

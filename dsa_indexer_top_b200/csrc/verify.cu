@@ -26,13 +26,14 @@ namespace {
 // to every CTA of the cluster, the one whose segment crosses the target reads that
 // segment (an eighth of its share, still in L2) once more and finds the token by a scan of
 // per-thread runs.  Bound by memory: 4 or 2 bytes per entry and row, and by latency
-// (three dependent round trips) for few requests.  Measured (one B200): 96 requests, 4
-// drafts, vocabulary 131071 in float32 33 us (101 MB, 3.0 TB/s; float64 conversions and
-// sums share the issue slots); one CTA per request 252 us; 512 threads, two CTAs per SM
-// 43 us.  5 requests, 32000 in bf16: 10 us (one CTA per request 34).
+// (three dependent round trips) for few requests.  Measured (one B200): 96 requests, up
+// to 4 drafts, vocabulary 131071 in float32 33 us (66 MB: the draft's row is read where a
+// draft is rejected, some 30 of 96; 2.0 TB/s; float64 conversions and sums share the
+// issue slots); one CTA per request 252 us; 512 threads, two CTAs per SM 43 us.  5
+// requests, 32000 in bf16: 9.9 us (one CTA per request 34).
 constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
-constexpr int kVerPerSm = 4;  // CTAs per SM (64 registers a thread)
+constexpr int kVerPerSm = 4;  // CTAs per SM (they fit with up to 64 registers a thread)
 constexpr int kVerMaxCluster = 8;
 constexpr int kVerUnroll = 8;  // loads of a row in flight per thread
 
