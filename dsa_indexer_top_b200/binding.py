@@ -195,13 +195,13 @@ class _CStruct:
             object.__setattr__(self, "_cs", cs)
         return cs
 
-    def checked(self, check, other=None):
-        """The value of check(self, other), found once and kept until a field of either is assigned."""
+    def checked(self, check):
+        """The value of check(self), found once and kept until a field is assigned."""
         was = self.__dict__.get("_ok")
-        if was is None or was[0] is not self.c() or (other is not None and was[1] is not other.c()):
-            was = (self.c(), other and other.c(), check(self) if other is None else check(self, other))
+        if was is None or was[0] is not self.c():
+            was = (self.c(), check(self))
             object.__setattr__(self, "_ok", was)
-        return was[2]
+        return was[1]
 
 
 @dataclass
@@ -567,7 +567,7 @@ def _paged_writer(writer: CacheWriter) -> int:
     if writer.kv is not None and writer.k_idx is not None and writer.kv.shape[:2] != writer.k_idx.shape[:2]:
         raise ValueError("kv and k_idx hold the same pages and rows")
     _int32(writer.tok_pos)
-    if writer.tok_pos.numel() != n:
+    if writer.tok_pos.numel() < n:
         raise ValueError("tok_pos holds one position per token")
     for t, dtype, size in ((writer.h, torch.bfloat16, 0), (writer.w, torch.bfloat16, 704 * hidden),
                            (writer.kv, torch.bfloat16, 0), (writer.k_idx, torch.bfloat16, 0),
@@ -595,20 +595,25 @@ def dsa_write_paged_rows(writer: CacheWriter, slot_map: torch.Tensor, ws: torch.
            "dsa_write_paged_rows")
 
 
-def _paged_shapes(batch: PagedBatch, mla: Mla) -> int:
-    kv, q, out, lse, n = mla.kv, mla.q, mla.out, mla.lse, batch.n_tok
-    if kv.dim() != 3 or kv.shape[0] < batch.n_pages or kv.shape[1] < batch.page_rows:
+def _paged_pool(mla: Mla):
+    """The tensors' device, the pool's pages and rows per page, and the tokens that there is room for."""
+    kv, q, out, lse, heads = mla.kv, mla.q, mla.out, mla.lse, mla.q.shape[1]
+    if kv.dim() != 3:
         raise ValueError("the pool is [n_pages, page_rows, row]")
-    if q.shape[0] < n or out.shape[0] < n or (lse is not None and lse.shape[0] < n):
-        raise ValueError("queries and outputs hold n_tok rows")
     if kv.dtype not in (q.dtype, torch.uint8) or out.dtype != q.dtype or (lse is not None and lse.dtype != torch.float32):
         raise TypeError("queries, outputs and the pool are of one type (a uint8 pool: packed FP8 rows), the lse float32")
     if not (q.is_contiguous() and out.is_contiguous() and (lse is None or lse.is_contiguous())) or kv.stride(2) != 1:
         raise TypeError("queries, outputs, the lse and the pool's rows are contiguous")
-    if (kv.shape[2] < (DSA_MLA_FP8_ROW_BYTES if kv.dtype == torch.uint8 else q.shape[2]) or mla.d_latent > q.shape[2]
-            or out.numel() < n * q.shape[1] * mla.d_latent or (lse is not None and lse.numel() < n * q.shape[1])):
-        raise ValueError("pool rows, outputs or the lse are too small for the queries")
-    return _device_of(batch.block_table, batch.q_begin, batch.seq_len, q, kv, out, lse)
+    if kv.shape[2] < (DSA_MLA_FP8_ROW_BYTES if kv.dtype == torch.uint8 else q.shape[2]) or mla.d_latent > q.shape[2]:
+        raise ValueError("pool rows or d_latent do not fit the queries")
+    room = min(q.shape[0], out.shape[0], out.numel() // max(1, heads * mla.d_latent))
+    if lse is not None:
+        room = min(room, lse.shape[0], lse.numel() // max(1, heads))
+    return _device_of(q, kv, out, lse), kv.shape[0], kv.shape[1], room
+
+
+def _batch_device(batch: PagedBatch) -> int:
+    return _device_of(batch.block_table, batch.q_begin, batch.seq_len)
 
 
 def dsa_paged_mla_workspace_bytes(batch: PagedBatch, mla: Mla) -> int:
@@ -616,7 +621,15 @@ def dsa_paged_mla_workspace_bytes(batch: PagedBatch, mla: Mla) -> int:
 
 
 def dsa_paged_mla(batch: PagedBatch, mla: Mla, ws: torch.Tensor, stream=None):
-    dev, bc, mc = batch.checked(_paged_shapes, mla), batch.c(), mla.c()
+    dev, pages, rows, room = mla.checked(_paged_pool)
+    if pages < batch.n_pages or rows < batch.page_rows:
+        raise ValueError("the pool is [n_pages, page_rows, row]")
+    if room < batch.n_tok:
+        raise ValueError("queries and outputs hold n_tok rows")
+    at = batch.checked(_batch_device)
+    if at != dev and at >= 0:
+        raise ValueError(f"tensors on cuda:{dev} and cuda:{at}")
+    bc, mc = batch.c(), mla.c()
     _check(lib().dsa_paged_mla(ctypes.byref(bc), ctypes.byref(mc), _ptr(ws), ws.nbytes, _stream_on(dev, ws, stream)),
            "dsa_paged_mla")
 

@@ -39,9 +39,26 @@ def test_a_descriptor_is_checked_again_when_it_changes():
         with pytest.raises(TypeError):
             B.dsa_paged_mla(batch, mla, WS)
     mla.lse = None
-    batch.n_tok = 4
-    with pytest.raises(ValueError, match="n_tok"):
+    with pytest.raises(ValueError, match="GPU"):     # (host tensors: everything else fits)
         B.dsa_paged_mla(batch, mla, WS)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(n_tok=4), dict(n_pages=10), dict(page_rows=17)])
+def test_a_batch_that_one_layer_has_no_room_for(cuda_ok, kw):
+    """Layers share a batch; each one's tensors are held to it."""
+    dev = lambda m: B.Mla(m.q.cuda(), m.kv.cuda(), m.out.cuda(), 512, 0.1, m.lse.cuda())
+    batch = _batch(block_table=i32(2, 4).cuda(), q_begin=i32(3).cuda(), seq_len=i32(2).cuda())
+    layers = [dev(_mla()), dev(_mla())]
+    ws = B.paged_workspace(batch, layers[0])
+    for layer in layers:
+        B.dsa_paged_mla(batch, layer, ws)          # (no sequence has tokens: nothing is read)
+    for k, v in kw.items():
+        setattr(batch, k, v)
+    for layer in layers:
+        with pytest.raises(ValueError):
+            B.dsa_paged_mla(batch, layer, ws)
+    torch.cuda.synchronize()
 
 
 def _writer(**kw):
